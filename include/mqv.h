@@ -63,7 +63,8 @@ typedef enum {
 
 typedef enum { MQV_NVFP4 = 0 /* E2M1 elements */, MQV_NVFP6 = 1 /* E2M3 */ } mqv_format;
 typedef enum { MQV_RNE = 0, MQV_SR = 1 } mqv_rounding;
-typedef enum { MQV_OP_FWD = 1, MQV_OP_WGRAD = 2, MQV_OP_DGRAD = 3, MQV_OP_FWD_BLOCKSCALED = 4 } mqv_op;
+typedef enum { MQV_OP_FWD = 1, MQV_OP_WGRAD = 2, MQV_OP_DGRAD = 3, MQV_OP_FWD_BLOCKSCALED = 4,
+               MQV_OP_ACT_GRAD = 5 } mqv_op;
 
 /* Shape of one convolution layer (the pages' N, Cin, Cout, H, W, Kh, Kw,
  * stride, pad, format).  Requirements: all > 0 (pad >= 0), Cin, Cout and N
@@ -385,6 +386,90 @@ mqv_status mqv_dw_wgrad_workspace_size(const mqv_dw_desc* d, size_t* bytes);
  * added in a fixed order.  ws: at least mqv_dw_wgrad_workspace_size bytes. */
 mqv_status mqv_dw_wgrad(const mqv_dw_desc* d, const void* gy, const void* x, float* gw, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* ---- Layers in BF16 beside the depthwise ones: layer norm over the
+ * channels and the linear (pointwise) layer, forward and backward.  Tensors
+ * are [P][C][N] with the batch index n fastest: P = H·W positions for the
+ * channel-batch-first layout of the convolutions, N = 1 for rows of tokens
+ * ([P][C], P tokens of C channels).  "Columns" are the P·N pairs (p, n).
+ * Element types (mqv_dtype) are given per tensor: fp32, or bfloat16 bit
+ * patterns; parameters (gamma, beta, bias), statistics and the gradients of
+ * parameters are fp32.  All sums are fp32, in a fixed order: results repeat
+ * run to run.
+ * Validation, common to all of them: C (Cin, Cout) and N positive, P >= 0
+ * (P = 0: nothing is read, gradients of parameters are written as zeros),
+ * fewer than 2^31 columns, every buffer 16-byte aligned device memory the
+ * caller owns; no written buffer may overlap another buffer of the call
+ * unless stated.  Failures return before anything is launched.  Calls that
+ * overlap on the GPU need workspaces of their own. */
+typedef enum { MQV_F32 = 0, MQV_BF16 = 1 } mqv_dtype;
+typedef enum { MQV_ACT_NONE = 0, MQV_ACT_RELU = 1, MQV_ACT_GELU = 2 /* z·Phi(z), by erf */,
+               MQV_ACT_SILU = 3 } mqv_act;
+
+/* Layer norm of [P][C][N] over C (at most 16384 channels); eps finite, >= 0. */
+typedef struct {
+  int64_t P, C, N;
+  float eps;
+  int32_t reserved; /* must be 0 */
+} mqv_ln_desc;
+
+/* y = (x - mean)·rstd·gamma + beta with mean = sum_c x / C and rstd =
+ * (sum_c (x - mean)^2 / C + eps)^(-1/2) of each column.  gamma, beta: [C],
+ * NULL for 1 and 0.  mean, rstd: [P][N], both NULL if not kept.  y may be x
+ * itself when their types are the same.  A NaN or infinity in a column makes
+ * that column NaN and no other. */
+mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const float* gamma, const float* beta,
+                      void* y, int32_t y_type, float* mean, float* rstd, void* stream);
+
+/* Workspace bytes of mqv_ln_bwd with parameter gradients (partial sums per
+ * block).  Host-only. */
+mqv_status mqv_ln_bwd_workspace_size(const mqv_ln_desc* d, size_t* bytes);
+
+/* Gradients of mqv_ln_fwd from gy, the input x and the kept mean and rstd:
+ * with xh = (x - mean)·rstd and g = gamma·gy (gamma NULL: 1),
+ *   gx = rstd·(g - sum_c g / C - xh·sum_c (g·xh) / C),
+ *   ggamma[c] = sum_{p,n} gy·xh, gbeta[c] = sum_{p,n} gy.
+ * ggamma and gbeta: both NULL if not wanted (ws may then be NULL).  gx may be
+ * gy itself when their types are the same. */
+mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, const void* x, int32_t x_type,
+                      const float* mean, const float* rstd, const float* gamma, void* gx, int32_t gx_type,
+                      float* ggamma, float* gbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* Linear layer Cin -> Cout over the channels of [P][Cin][N]: for tokens
+ * (N = 1) y = x·w^T, for pixels a 1 x 1 convolution.  w: bfloat16
+ * [Cout][Cin]; x and gz bfloat16 [P][Cin][N] and [P][Cout][N]. */
+typedef struct {
+  int64_t P, Cin, Cout, N;
+  int32_t act;      /* mqv_act */
+  int32_t reserved; /* must be 0 */
+} mqv_lin_desc;
+
+/* Workspace bytes of mqv_lin_fwd, mqv_lin_wgrad, mqv_lin_dgrad or
+ * mqv_lin_act_grad (op = MQV_OP_FWD, MQV_OP_WGRAD, MQV_OP_DGRAD or
+ * MQV_OP_ACT_GRAD); 0 where none is needed.  Host-only. */
+mqv_status mqv_lin_workspace_size(const mqv_lin_desc* d, int32_t op, size_t* bytes);
+
+/* z = w·x + bias over the channels, y = act(z) + residual, one fp32 sum per
+ * output, rounded once to y's type.  bias: [Cout] or NULL; residual: of y's
+ * shape and type, or NULL, and may be y itself; z: bfloat16 [P][Cout][N] that
+ * keeps the pre-activation for mqv_lin_act_grad, or NULL. */
+mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, const float* bias, const void* residual,
+                       void* z, void* y, int32_t y_type, void* ws, size_t ws_bytes, void* stream);
+
+/* gz = gy·act'(z), rounded to bfloat16, and gbias[co] = sum_{p,n} of the
+ * unrounded gz.  (The residual's gradient is gy.)  z: as mqv_lin_fwd kept it,
+ * not read when act is MQV_ACT_NONE; gz or gbias may be NULL, not both; gz
+ * may be gy itself when gy is bfloat16. */
+mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_type, const void* z, void* gz,
+                            float* gbias, void* ws, size_t ws_bytes, void* stream);
+
+/* gx[ci][j] = sum_co w[co][ci]·gz[co][j], in gx's type.  (d->act is not used.) */
+mqv_status mqv_lin_dgrad(const mqv_lin_desc* d, const void* w, const void* gz, void* gx, int32_t gx_type, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* gw[co][ci] = sum_j gz[co][j]·x[ci][j] over the columns j, fp32 [Cout][Cin]. */
+mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, float* gw, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* Synchronizes `stream`, then reports and clears the device error word that
  * bounded waits inside the conv kernels set when they give up

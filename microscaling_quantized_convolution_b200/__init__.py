@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libmqv.so")
 
 NVFP4, NVFP6 = 0, 1
 RNE, SR = 0, 1
-OP_FWD, OP_WGRAD, OP_DGRAD, OP_FWD_BLOCKSCALED = 1, 2, 3, 4
+OP_FWD, OP_WGRAD, OP_DGRAD, OP_FWD_BLOCKSCALED, OP_ACT_GRAD = 1, 2, 3, 4, 5
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
+ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "silu": ACT_SILU}
 FORMATS = {"nvfp4": NVFP4, "nvfp6": NVFP6, NVFP4: NVFP4, NVFP6: NVFP6}
 
 
@@ -59,6 +61,16 @@ class DwDesc(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("C", ctypes.c_int64), ("H", ctypes.c_int64), ("W", ctypes.c_int64),
                 ("Kh", ctypes.c_int64), ("Kw", ctypes.c_int64), ("stride", ctypes.c_int64),
                 ("pad", ctypes.c_int64), ("reserved", ctypes.c_int32), ("reserved2", ctypes.c_int32)]
+
+
+class LnDesc(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int64), ("C", ctypes.c_int64), ("N", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class LinDesc(ctypes.Structure):
+    _fields_ = [("P", ctypes.c_int64), ("Cin", ctypes.c_int64), ("Cout", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -133,6 +145,26 @@ _SIGS = {
     "mqv_dw_wgrad_workspace_size": (ctypes.c_int, [ctypes.POINTER(DwDesc), ctypes.POINTER(ctypes.c_size_t)]),
     "mqv_dw_wgrad": (ctypes.c_int, [ctypes.POINTER(DwDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mqv_ln_fwd": (ctypes.c_int, [ctypes.POINTER(LnDesc), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_void_p]),
+    "mqv_ln_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(LnDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "mqv_ln_bwd": (ctypes.c_int, [ctypes.POINTER(LnDesc), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mqv_lin_workspace_size": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_int32,
+                                              ctypes.POINTER(ctypes.c_size_t)]),
+    "mqv_lin_fwd": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                   ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mqv_lin_act_grad": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
+    "mqv_lin_dgrad": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mqv_lin_wgrad": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -600,4 +632,255 @@ def dw_wgrad(d: DwDesc, gy: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | No
         ws = torch.empty(dw_wgrad_workspace_bytes(d), dtype=torch.uint8, device=x.device)
     _check(lib().mqv_dw_wgrad(ctypes.byref(d), gy.data_ptr(), x.data_ptr(), gw.data_ptr(), ws.data_ptr(),
                               ws.numel(), _stream(stream)))
+    return gw
+
+
+# ------------------------- layer norm and linear layers in BF16 or fp32
+#
+# Tensors are [P][C][N], N fastest (N = 1: rows of tokens; a [P][C] tensor
+# does).  A call runs on its tensors' device, on `stream` or that device's
+# current stream; outputs and workspaces that it allocates belong to that
+# stream, so their memory is not handed out again before the stream is done
+# with it.
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class _OnDevice:
+    """Makes `device` (and `stream`, if one is given) current for a call and
+    holds the stream's handle.  The common case, the current device and no
+    stream given, costs two look-ups."""
+    __slots__ = ("handle", "_dev", "_ctx")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self._dev = self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self._dev = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        elif self._dev is not None:
+            self._dev.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        elif self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+def _operand(t, name: str, n: int, device, dtype=None):
+    """Checks a tensor of n elements on `device`: the C ABI takes no tensor
+    sizes, so a short tensor would be read or written out of bounds there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is None:
+        if t.dtype not in _TYPES:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name}: {t.numel()} elements, the descriptor needs {n}")
+    return t.data_ptr()
+
+
+def _optional(t, name: str, n: int, device, dtype=None):
+    return None if t is None else _operand(t, name, n, device, dtype)
+
+
+def _result(t, name: str, shape, dtype, device):
+    """(tensor, pointer) of an output: `t` checked, or a new tensor."""
+    if t is None:
+        if dtype not in _TYPES:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    n = 1
+    for s in shape:
+        n *= s
+    return t, _operand(t, name, n, device, dtype)
+
+
+def _layer_ws(ws, need: int, device):
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def ln_desc(P, C, N=1, eps=1e-5) -> LnDesc:
+    """Descriptor of a layer norm over the C channels of a [P][C][N] tensor."""
+    return LnDesc(P, C, N, eps, 0)
+
+
+def ln_bwd_workspace_bytes(d: LnDesc) -> int:
+    """Workspace bytes of ln_bwd; raises MqvError for an invalid descriptor."""
+    b = ctypes.c_size_t()
+    _check(lib().mqv_ln_bwd_workspace_size(ctypes.byref(d), ctypes.byref(b)))
+    return b.value
+
+
+def ln_fwd(d: LnDesc, x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+           y: torch.Tensor | None = None, y_dtype=None, mean: torch.Tensor | None = None,
+           rstd: torch.Tensor | None = None, stats: bool = True, stream=None):
+    """(y, mean, rstd): the layer norm of x [P][C][N] (see mqv_ln_fwd).  y is
+    of y_dtype (x's type if not given); mean and rstd [P][N] fp32 are kept for
+    ln_bwd, or None with stats=False.  gamma, beta: fp32 [C] or None."""
+    ln_bwd_workspace_bytes(d)
+    dev = x.device
+    n, cols = d.P * d.C * d.N, d.P * d.N
+    xp = _operand(x, "x", n, dev)
+    gp, bp = _optional(gamma, "gamma", d.C, dev, torch.float32), _optional(beta, "beta", d.C, dev, torch.float32)
+    with _OnDevice(dev, stream) as on:
+        if y is not None and y_dtype is None:
+            y_dtype = y.dtype
+        y, yp = _result(y, "y", (d.P, d.C, d.N), y_dtype or x.dtype, dev)
+        mp = rp = None
+        if stats or mean is not None or rstd is not None:
+            mean, mp = _result(mean, "mean", (d.P, d.N), torch.float32, dev)
+            rstd, rp = _result(rstd, "rstd", (d.P, d.N), torch.float32, dev)
+        _check(lib().mqv_ln_fwd(ctypes.byref(d), xp, _TYPES[x.dtype], gp, bp, yp, _TYPES[y.dtype], mp, rp, on.handle))
+    return y, mean, rstd
+
+
+def ln_bwd(d: LnDesc, gy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+           gamma: torch.Tensor | None = None, gx: torch.Tensor | None = None, gx_dtype=None,
+           ggamma: torch.Tensor | None = None, gbeta: torch.Tensor | None = None, param_grads: bool = True,
+           ws: torch.Tensor | None = None, stream=None):
+    """(gx, ggamma, gbeta) of ln_fwd (see mqv_ln_bwd); gx is of gx_dtype (x's
+    type if not given), ggamma and gbeta fp32 [C], None with param_grads=False."""
+    need = ln_bwd_workspace_bytes(d)
+    dev = x.device
+    n, cols = d.P * d.C * d.N, d.P * d.N
+    gyp, xp = _operand(gy, "gy", n, dev), _operand(x, "x", n, dev)
+    mp = _operand(mean, "mean", cols, dev, torch.float32)
+    rp = _operand(rstd, "rstd", cols, dev, torch.float32)
+    gp = _optional(gamma, "gamma", d.C, dev, torch.float32)
+    with _OnDevice(dev, stream) as on:
+        if gx is not None and gx_dtype is None:
+            gx_dtype = gx.dtype
+        gx, gxp = _result(gx, "gx", (d.P, d.C, d.N), gx_dtype or x.dtype, dev)
+        ggp = gbp = wp = None
+        wn = 0
+        if param_grads or ggamma is not None or gbeta is not None:
+            ggamma, ggp = _result(ggamma, "ggamma", (d.C,), torch.float32, dev)
+            gbeta, gbp = _result(gbeta, "gbeta", (d.C,), torch.float32, dev)
+            ws, wp, wn = _layer_ws(ws, need, dev)
+        _check(lib().mqv_ln_bwd(ctypes.byref(d), gyp, _TYPES[gy.dtype], xp, _TYPES[x.dtype], mp, rp, gp, gxp,
+                                _TYPES[gx.dtype], ggp, gbp, wp, wn, on.handle))
+    return gx, ggamma, gbeta
+
+
+def lin_desc(P, Cin, Cout, N=1, act="none") -> LinDesc:
+    """Descriptor of a linear layer Cin -> Cout over the channels of a
+    [P][Cin][N] tensor; act: "none", "relu", "gelu" (by erf) or "silu"."""
+    return LinDesc(P, Cin, Cout, N, ACTS[act] if act in ACTS else int(act), 0)
+
+
+def lin_workspace_bytes(d: LinDesc, op: int) -> int:
+    """Workspace bytes of a linear pass (OP_FWD, OP_WGRAD, OP_DGRAD or
+    OP_ACT_GRAD); raises MqvError for an invalid descriptor."""
+    b = ctypes.c_size_t()
+    _check(lib().mqv_lin_workspace_size(ctypes.byref(d), op, ctypes.byref(b)))
+    return b.value
+
+
+def lin_fwd(d: LinDesc, w: torch.Tensor, x: torch.Tensor, bias: torch.Tensor | None = None,
+            residual: torch.Tensor | None = None, y: torch.Tensor | None = None, y_dtype=None,
+            z: torch.Tensor | None = None, save_z: bool = False, ws: torch.Tensor | None = None, stream=None):
+    """(y, z): y [P][Cout][N] = act(w·x + bias) + residual over the channels
+    (see mqv_lin_fwd), of y_dtype (the residual's, else bfloat16, if not
+    given); z, the bfloat16 pre-activation that lin_act_grad takes, with
+    save_z=True (or into the z given), else None.  w: bfloat16 [Cout][Cin]."""
+    need = lin_workspace_bytes(d, OP_FWD)
+    dev = x.device
+    n = d.P * d.Cout * d.N
+    wtp = _operand(w, "w", d.Cout * d.Cin, dev, torch.bfloat16)
+    xp = _operand(x, "x", d.P * d.Cin * d.N, dev, torch.bfloat16)
+    bp = _optional(bias, "bias", d.Cout, dev, torch.float32)
+    if y_dtype is None:
+        y_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.bfloat16
+    rp = _optional(residual, "residual", n, dev, y_dtype)
+    with _OnDevice(dev, stream) as on:
+        shape = (d.P, d.Cout, d.N)
+        y, yp = _result(y, "y", shape, y_dtype, dev)
+        zp = None
+        if save_z or z is not None:
+            z, zp = _result(z, "z", shape, torch.bfloat16, dev)
+        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
+        _check(lib().mqv_lin_fwd(ctypes.byref(d), wtp, xp, bp, rp, zp, yp, _TYPES[y.dtype], wp, wn, on.handle))
+    return y, z
+
+
+def lin_act_grad(d: LinDesc, gy: torch.Tensor, z: torch.Tensor | None = None, gz: torch.Tensor | None = None,
+                 gbias: torch.Tensor | None = None, bias_grad: bool = True, ws: torch.Tensor | None = None,
+                 stream=None):
+    """(gz, gbias): gz = gy·act'(z) in bfloat16 and its fp32 sum over the
+    columns, gbias [Cout] (None with bias_grad=False; see mqv_lin_act_grad).
+    With act "none", a bfloat16 gy and no gz given, gz is gy itself."""
+    need = lin_workspace_bytes(d, OP_ACT_GRAD)
+    dev = gy.device
+    n = d.P * d.Cout * d.N
+    gyp = _operand(gy, "gy", n, dev)
+    zp = None
+    if d.act != ACT_NONE:
+        if z is None:
+            raise ValueError("z, the pre-activation that lin_fwd kept, is needed for this activation")
+        zp = _operand(z, "z", n, dev, torch.bfloat16)
+    bias_grad = bias_grad or gbias is not None
+    with _OnDevice(dev, stream) as on:
+        gzp = gbp = wp = None
+        wn = 0
+        if d.act == ACT_NONE and gz is None and gy.dtype == torch.bfloat16:
+            gz = gy
+        else:
+            gz, gzp = _result(gz, "gz", (d.P, d.Cout, d.N), torch.bfloat16, dev)
+        if bias_grad:
+            gbias, gbp = _result(gbias, "gbias", (d.Cout,), torch.float32, dev)
+            ws, wp, wn = _layer_ws(ws, need, dev)
+        if gzp is not None or gbp is not None:
+            _check(lib().mqv_lin_act_grad(ctypes.byref(d), gyp, _TYPES[gy.dtype], zp, gzp, gbp, wp, wn, on.handle))
+    return gz, gbias
+
+
+def lin_dgrad(d: LinDesc, w: torch.Tensor, gz: torch.Tensor, gx: torch.Tensor | None = None, gx_dtype=None,
+              ws: torch.Tensor | None = None, stream=None):
+    """gx [P][Cin][N] = w^T·gz over the channels (see mqv_lin_dgrad), of
+    gx_dtype (bfloat16 if not given)."""
+    need = lin_workspace_bytes(d, OP_DGRAD)
+    dev = gz.device
+    wtp = _operand(w, "w", d.Cout * d.Cin, dev, torch.bfloat16)
+    gp = _operand(gz, "gz", d.P * d.Cout * d.N, dev, torch.bfloat16)
+    with _OnDevice(dev, stream) as on:
+        if gx is not None and gx_dtype is None:
+            gx_dtype = gx.dtype
+        gx, gxp = _result(gx, "gx", (d.P, d.Cin, d.N), gx_dtype or torch.bfloat16, dev)
+        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
+        _check(lib().mqv_lin_dgrad(ctypes.byref(d), wtp, gp, gxp, _TYPES[gx.dtype], wp, wn, on.handle))
+    return gx
+
+
+def lin_wgrad(d: LinDesc, gz: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | None = None,
+              ws: torch.Tensor | None = None, stream=None):
+    """gw [Cout][Cin] fp32 = sum over the columns of gz·x^T (see mqv_lin_wgrad)."""
+    need = lin_workspace_bytes(d, OP_WGRAD)
+    dev = x.device
+    gp = _operand(gz, "gz", d.P * d.Cout * d.N, dev, torch.bfloat16)
+    xp = _operand(x, "x", d.P * d.Cin * d.N, dev, torch.bfloat16)
+    with _OnDevice(dev, stream) as on:
+        gw, gwp = _result(gw, "gw", (d.Cout, d.Cin), torch.float32, dev)
+        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
+        _check(lib().mqv_lin_wgrad(ctypes.byref(d), gp, xp, gwp, wp, wn, on.handle))
     return gw

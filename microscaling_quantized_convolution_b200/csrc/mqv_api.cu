@@ -12,6 +12,7 @@
 #include <string>
 
 #include "mqv.h"
+#include "mqv_host.h"
 #include "mqv_conv_common.cuh"
 #include "mqv_conv_kernels.cuh"
 #include "mqv_conv_halo.cuh"
@@ -23,11 +24,14 @@
 #include "mqv_quantize.cuh"
 #include "mqv_replay.cuh"
 
-namespace {
+namespace mqv {
 
-using namespace mqv;
+// Device word that bounded waits set on timeout (see mqv_ptx.cuh).
+static __device__ uint32_t g_device_error;
 
-thread_local char g_msg[512] = "";
+static thread_local char g_msg[512] = "";
+static uint32_t* g_err_ptr[kMaxDevices] = {};
+static std::mutex g_err_mu;
 
 mqv_status fail(mqv_status st, const char* fmt, ...) {
   va_list ap;
@@ -46,15 +50,6 @@ mqv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(MQV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Device word that bounded waits set on timeout (see mqv_ptx.cuh).
-__device__ uint32_t g_device_error;
-
-constexpr int kMaxDevices = 64;
-uint32_t* g_err_ptr[kMaxDevices] = {};
-std::mutex g_err_mu;
-
 mqv_status device_error_word(uint32_t** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -70,6 +65,12 @@ mqv_status device_error_word(uint32_t** out) {
   *out = g_err_ptr[dev];
   return MQV_OK;
 }
+
+}  // namespace mqv
+
+namespace {
+
+using namespace mqv;
 
 // ------------------------------------------------------------ quantize geometry
 

@@ -1,0 +1,468 @@
+// C ABI of the BF16 layers around the quantized convolutions (declared in
+// include/mqv.h): layer norm and the linear layer.  Argument validation and
+// launch geometry; the arithmetic is in mqv_norm.cuh and mqv_linear.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+
+#include "mqv.h"
+#include "mqv_host.h"
+#include "mqv_linear.cuh"
+#include "mqv_norm.cuh"
+
+namespace {
+
+using namespace mqv;
+
+constexpr int kSms = 148;
+constexpr int64_t kMaxChannels = 16384;             // layer norm: a position's channels in one block's registers
+constexpr int64_t kMaxElements = int64_t{1} << 40;
+constexpr int64_t kMaxColumns = (int64_t{1} << 31) - 1;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t b) { return ceil_div(b, 256) * 256; }
+int64_t type_size(int32_t t) { return t == MQV_BF16 ? 2 : 4; }
+
+mqv_status check_type(int32_t t, const char* name) {
+  if (t != MQV_F32 && t != MQV_BF16) return fail(MQV_ERR_INVALID_ARG, "%s: unknown element type %d", name, t);
+  return MQV_OK;
+}
+
+// A device buffer of a call: what it is, where, how many bytes; `out` when the
+// call writes it, `need` when it may not be null.
+struct Buf {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+  bool out, need;
+};
+
+// Pointers present and 16-byte aligned, no written buffer overlapping another,
+// except that `alias` may be exactly the buffer of `of` (element-wise reads
+// and writes of the same element by one thread).
+mqv_status check_buffers(std::initializer_list<Buf> bufs, const char* alias = nullptr, const char* of = nullptr) {
+  for (const Buf& b : bufs) {
+    if (b.need && b.bytes > 0 && !b.p) return fail(MQV_ERR_INVALID_ARG, "%s: null pointer", b.name);
+    if (b.p && !aligned16(b.p)) return fail(MQV_ERR_INVALID_ARG, "%s must be 16-byte aligned", b.name);
+  }
+  for (const Buf& a : bufs)
+    for (const Buf& b : bufs) {
+      if (!a.out || &a == &b || !a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+      if (x >= y + b.bytes || y >= x + a.bytes) continue;
+      if (alias && x == y && a.bytes == b.bytes && !b.out && a.name == alias && b.name == of) continue;
+      return fail(MQV_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    }
+  return MQV_OK;
+}
+
+mqv_status check_workspace(const void* ws, size_t have, int64_t need) {
+  if (need > 0 && (!ws || have < static_cast<size_t>(need) || !aligned16(ws)))
+    return fail(MQV_ERR_WORKSPACE, "workspace of %lld bytes required", (long long)need);
+  return MQV_OK;
+}
+
+mqv_status launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ok() : cuda_fail(e, what);
+}
+
+void launch_column_sum(const float* part, int64_t rows, int64_t n, int pairs, float* out0, float* out1,
+                       cudaStream_t st) {
+  column_sum_kernel<<<(unsigned)ceil_div(n * pairs, 32), 256, 0, st>>>(part, (int)rows, n, pairs, out0, out1);
+}
+
+// ------------------------------------------------------------- layer norm
+
+// Launch geometry of one direction: vector width, vectors per thread, threads
+// per block, and (N > 1) the tile.
+struct LnPlan {
+  int v, k, threads;
+  int tn, tiles, lanes, rows;
+  int64_t units;                 // rows or tiles
+  int64_t bwd_blocks;
+};
+
+mqv_status plan_ln(const mqv_ln_desc* d, LnPlan* pl) {
+  if (!d) return fail(MQV_ERR_INVALID_ARG, "null descriptor");
+  if (d->P < 0 || d->C <= 0 || d->N <= 0 || d->reserved)
+    return fail(MQV_ERR_INVALID_ARG, "layer norm of [%lld][%lld][%lld]: P >= 0, C and N > 0, reserved 0 required",
+                (long long)d->P, (long long)d->C, (long long)d->N);
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return fail(MQV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (d->C > kMaxChannels)
+    return fail(MQV_ERR_UNSUPPORTED, "%lld channels: at most %lld", (long long)d->C, (long long)kMaxChannels);
+  if (d->N > kMaxColumns || d->P > kMaxColumns / d->N || (d->P > 0 && d->C > kMaxElements / (d->P * d->N)))
+    return fail(MQV_ERR_UNSUPPORTED, "tensor [%lld][%lld][%lld] too large", (long long)d->P, (long long)d->C,
+                (long long)d->N);
+  if (d->N == 1) {
+    // 8 values a thread up to 2048 channels, 16 above
+    const int e = d->C <= 2048 ? 8 : 16;
+    pl->v = d->C % 8 == 0 ? 8 : 1;
+    pl->k = e / pl->v;
+    pl->threads = (int)(ceil_div(ceil_div(d->C, e), 32) * 32);
+    pl->units = d->P;
+    pl->tn = pl->tiles = pl->lanes = pl->rows = 0;
+  } else {
+    // 16 values a thread; the widest vectors and the widest tile (up to 64
+    // batch items) whose channels fit in one block
+    pl->threads = 0;
+    for (int v : {8, 4, 1}) {
+      if (d->N % v) continue;
+      const int k = 16 / v;
+      for (int64_t tiles = ceil_div(d->N, 64);; tiles *= 2) {
+        const int64_t tn = ceil_div(ceil_div(d->N, tiles), v) * v;
+        const int64_t lanes = tn / v, threads = ceil_div(lanes * ceil_div(d->C, k), 32) * 32;
+        if (threads <= kLnMaxThreads) {
+          pl->v = v;
+          pl->k = k;
+          pl->threads = (int)threads;
+          pl->tn = (int)tn;
+          pl->tiles = (int)ceil_div(d->N, tn);
+          pl->lanes = (int)lanes;
+          pl->rows = (int)(threads / lanes);
+          break;
+        }
+        if (tn <= v) break;
+      }
+      if (pl->threads) break;
+    }
+    if (!pl->threads) return fail(MQV_ERR_UNSUPPORTED, "%lld channels", (long long)d->C);
+    pl->units = d->P * pl->tiles;
+  }
+  pl->bwd_blocks = std::min<int64_t>(pl->units, (int64_t)kSms * std::max(1, 1024 / pl->threads));
+  return MQV_OK;
+}
+
+template <bool BWD, int V, int K, int T>
+void launch_ln_t(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+  const unsigned grid = (unsigned)(BWD ? pl.bwd_blocks : pl.units);
+  if (rows) {
+    if (BWD)
+      ln_bwd_row_kernel<V, K, T><<<grid, pl.threads, 0, st>>>(a);
+    else
+      ln_fwd_row_kernel<V, K, T><<<grid, pl.threads, 0, st>>>(a);
+  } else {
+    const size_t smem = (size_t)pl.threads * std::max(V, 2) * sizeof(float);
+    if (BWD)
+      ln_bwd_tile_kernel<V, K, T><<<grid, pl.threads, smem, st>>>(a);
+    else
+      ln_fwd_tile_kernel<V, K, T><<<grid, pl.threads, smem, st>>>(a);
+  }
+}
+
+template <bool BWD, int V, int K>
+void launch_ln_k(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+  if (pl.threads <= kLnFewThreads)
+    launch_ln_t<BWD, V, K, kLnFewThreads>(a, pl, rows, st);
+  else
+    launch_ln_t<BWD, V, K, kLnMaxThreads>(a, pl, rows, st);
+}
+
+template <bool BWD>
+void launch_ln(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+  if (pl.v == 8 && pl.k == 1) launch_ln_k<BWD, 8, 1>(a, pl, rows, st);
+  if (pl.v == 8 && pl.k == 2) launch_ln_k<BWD, 8, 2>(a, pl, rows, st);
+  if (pl.v == 4) launch_ln_k<BWD, 4, 4>(a, pl, rows, st);
+  if (pl.v == 1 && pl.k == 8) launch_ln_k<BWD, 1, 8>(a, pl, rows, st);
+  if (pl.v == 1 && pl.k == 16) launch_ln_k<BWD, 1, 16>(a, pl, rows, st);
+}
+
+LnArgs ln_args(const mqv_ln_desc* d, const LnPlan& pl, const void* x, int32_t x_type, const float* gamma) {
+  LnArgs a = {};
+  a.P = d->P;
+  a.N = d->N;
+  a.C = (int)d->C;
+  a.eps = d->eps;
+  a.gamma = gamma;
+  a.x = {x, x_type == MQV_BF16};
+  a.tn = pl.tn;
+  a.tiles = pl.tiles;
+  a.lanes = pl.lanes;
+  a.rows = pl.rows;
+  return a;
+}
+
+int64_t ln_bwd_ws(const mqv_ln_desc* d, const LnPlan& pl) { return align256(pl.bwd_blocks * 2 * d->C * 4); }
+
+// ----------------------------------------------------------- linear layer
+
+mqv_status check_lin(const mqv_lin_desc* d) {
+  if (!d) return fail(MQV_ERR_INVALID_ARG, "null descriptor");
+  if (d->P < 0 || d->Cin <= 0 || d->Cout <= 0 || d->N <= 0 || d->reserved)
+    return fail(MQV_ERR_INVALID_ARG,
+                "linear layer [%lld][%lld -> %lld][%lld]: P >= 0, Cin, Cout and N > 0, reserved 0 required",
+                (long long)d->P, (long long)d->Cin, (long long)d->Cout, (long long)d->N);
+  if (d->act < MQV_ACT_NONE || d->act > MQV_ACT_SILU) return fail(MQV_ERR_INVALID_ARG, "unknown activation %d", d->act);
+  const int64_t c = std::max(d->Cin, d->Cout);
+  if (c > (1 << 24) || d->N > kMaxColumns || d->P > kMaxColumns / d->N ||
+      (d->P > 0 && c > kMaxElements / (d->P * d->N)))
+    return fail(MQV_ERR_UNSUPPORTED, "linear layer [%lld][%lld -> %lld][%lld] too large", (long long)d->P,
+                (long long)d->Cin, (long long)d->Cout, (long long)d->N);
+  return MQV_OK;
+}
+
+struct ActGradPlan {
+  int v, lanes, rows;
+  int64_t tiles;
+  unsigned gx, gy;
+};
+
+ActGradPlan plan_act_grad(const mqv_lin_desc* d) {
+  ActGradPlan pl = {};
+  int64_t steps;
+  if (d->N == 1) {
+    pl.v = d->Cout % 8 == 0 ? 8 : 1;
+    pl.gx = (unsigned)ceil_div(d->Cout, 32 * pl.v);
+    steps = ceil_div(d->P, 8);
+  } else {
+    pl.v = d->N % 8 == 0 ? 8 : d->N % 4 == 0 ? 4 : 1;
+    pl.lanes = (int)std::min<int64_t>(ceil_div(d->N, pl.v), 256);
+    pl.rows = 256 / pl.lanes;
+    pl.tiles = ceil_div(d->N, (int64_t)pl.lanes * pl.v);
+    pl.gx = (unsigned)ceil_div(d->Cout, pl.rows);
+    steps = d->P * pl.tiles;
+  }
+  // about eight blocks an SM, four steps a block at least
+  const int64_t want = std::max<int64_t>(1, kSms * 8 / pl.gx);
+  pl.gy = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(steps, 4)));
+  return pl;
+}
+
+int64_t lin_ws(const mqv_lin_desc* d, int op) {
+  if (op == MQV_OP_ACT_GRAD) return align256((int64_t)plan_act_grad(d).gy * d->Cout * 4);
+  return 0;
+}
+
+Dim channel_dim(int64_t N) { return {int64_t{1} << 62, 0, N}; }
+Dim column_dim(int64_t C, int64_t N) { return {N, C * N, 1}; }
+
+mqv_status launch_gemm(const GemmArgs& g, cudaStream_t st) {
+  const int64_t blocks = ceil_div(g.M, 64) * ceil_div(g.N, 64);
+  if (blocks == 0) return ok();
+  gemm_simple_kernel<<<(unsigned)blocks, 256, 0, st>>>(g);
+  return launched("linear layer launch");
+}
+
+// D[channel][column] of a product over channels: rows are columns of the
+// tensor for token rows, channels otherwise, so that D's columns are
+// contiguous either way.
+void orient(GemmArgs* g, bool tokens, const void* w, Dim w_out, Dim w_k, int64_t out, const void* x, Dim x_col, Dim x_k,
+            int64_t cols, Dim d_ch, Dim d_col) {
+  const uint16_t *wp = static_cast<const uint16_t*>(w), *xp = static_cast<const uint16_t*>(x);
+  if (tokens) {
+    g->a = xp, g->a_row = x_col, g->a_k = x_k, g->b = wp, g->b_col = w_out, g->b_k = w_k;
+    g->M = cols, g->N = out, g->d_row = d_col, g->d_col = d_ch, g->bias_on_row = 0;
+  } else {
+    g->a = wp, g->a_row = w_out, g->a_k = w_k, g->b = xp, g->b_col = x_col, g->b_k = x_k;
+    g->M = out, g->N = cols, g->d_row = d_ch, g->d_col = d_col, g->bias_on_row = 1;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const float* gamma, const float* beta,
+                      void* y, int32_t y_type, float* mean, float* rstd, void* stream) {
+  LnPlan pl = {};
+  mqv_status st = plan_ln(d, &pl);
+  if (st || (st = check_type(x_type, "x")) || (st = check_type(y_type, "y"))) return st;
+  const int64_t cols = d->P * d->N, n = cols * d->C;
+  if (!mean != !rstd) return fail(MQV_ERR_INVALID_ARG, "mean and rstd: both or neither");
+  if ((st = check_buffers({{"x", x, n * type_size(x_type), false, true},
+                           {"gamma", gamma, d->C * 4, false, false},
+                           {"beta", beta, d->C * 4, false, false},
+                           {"y", y, n * type_size(y_type), true, true},
+                           {"mean", mean, cols * 4, true, false},
+                           {"rstd", rstd, cols * 4, true, false}},
+                          "y", "x")))
+    return st;
+  if (cols == 0) return ok();
+  LnArgs a = ln_args(d, pl, x, x_type, gamma);
+  a.beta = beta;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.out = {y, y_type == MQV_BF16};
+  launch_ln<false>(a, pl, d->N == 1, static_cast<cudaStream_t>(stream));
+  return launched("layer norm launch");
+}
+
+mqv_status mqv_ln_bwd_workspace_size(const mqv_ln_desc* d, size_t* bytes) {
+  LnPlan pl = {};
+  mqv_status st = plan_ln(d, &pl);
+  if (st) return st;
+  if (!bytes) return fail(MQV_ERR_INVALID_ARG, "null output pointer");
+  *bytes = (size_t)ln_bwd_ws(d, pl);
+  return ok();
+}
+
+mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, const void* x, int32_t x_type,
+                      const float* mean, const float* rstd, const float* gamma, void* gx, int32_t gx_type,
+                      float* ggamma, float* gbeta, void* ws, size_t ws_bytes, void* stream) {
+  LnPlan pl = {};
+  mqv_status st = plan_ln(d, &pl);
+  if (st || (st = check_type(gy_type, "gy")) || (st = check_type(x_type, "x")) || (st = check_type(gx_type, "gx")))
+    return st;
+  const int64_t cols = d->P * d->N, n = cols * d->C;
+  if (!ggamma != !gbeta) return fail(MQV_ERR_INVALID_ARG, "ggamma and gbeta: both or neither");
+  const int64_t need = ggamma ? ln_bwd_ws(d, pl) : 0;
+  if ((st = check_workspace(ws, ws_bytes, need))) return st;
+  if ((st = check_buffers({{"gy", gy, n * type_size(gy_type), false, true},
+                           {"x", x, n * type_size(x_type), false, true},
+                           {"mean", mean, cols * 4, false, true},
+                           {"rstd", rstd, cols * 4, false, true},
+                           {"gamma", gamma, d->C * 4, false, false},
+                           {"gx", gx, n * type_size(gx_type), true, true},
+                           {"ggamma", ggamma, d->C * 4, true, false},
+                           {"gbeta", gbeta, d->C * 4, true, false},
+                           {"ws", ws, need, true, false}},
+                          "gx", "gy")))
+    return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LnArgs a = ln_args(d, pl, x, x_type, gamma);
+  a.gy = {gy, gy_type == MQV_BF16};
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.out = {gx, gx_type == MQV_BF16};
+  a.part = ggamma ? static_cast<float*>(ws) : nullptr;
+  if (cols > 0) launch_ln<true>(a, pl, d->N == 1, s);
+  if (ggamma) launch_column_sum(a.part, pl.bwd_blocks, d->C, 2, ggamma, gbeta, s);
+  return launched("layer norm gradient launch");
+}
+
+mqv_status mqv_lin_workspace_size(const mqv_lin_desc* d, int32_t op, size_t* bytes) {
+  mqv_status st = check_lin(d);
+  if (st) return st;
+  if (op != MQV_OP_FWD && op != MQV_OP_WGRAD && op != MQV_OP_DGRAD && op != MQV_OP_ACT_GRAD)
+    return fail(MQV_ERR_INVALID_ARG, "unknown op %d", op);
+  if (!bytes) return fail(MQV_ERR_INVALID_ARG, "null output pointer");
+  *bytes = (size_t)lin_ws(d, op);
+  return ok();
+}
+
+mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, const float* bias, const void* residual,
+                       void* z, void* y, int32_t y_type, void* ws, size_t ws_bytes, void* stream) {
+  mqv_status st = check_lin(d);
+  if (st || (st = check_type(y_type, "y"))) return st;
+  const int64_t cols = d->P * d->N, n = cols * d->Cout, need = lin_ws(d, MQV_OP_FWD);
+  if ((st = check_workspace(ws, ws_bytes, need))) return st;
+  if ((st = check_buffers({{"w", w, d->Cout * d->Cin * 2, false, true},
+                           {"x", x, cols * d->Cin * 2, false, true},
+                           {"bias", bias, d->Cout * 4, false, false},
+                           {"residual", residual, n * type_size(y_type), false, false},
+                           {"z", z, n * 2, true, false},
+                           {"y", y, n * type_size(y_type), true, true},
+                           {"ws", ws, need, true, false}},
+                          "y", "residual")))
+    return st;
+  GemmArgs g = {};
+  orient(&g, d->N == 1, w, channel_dim(d->Cin), channel_dim(1), d->Cout, x, column_dim(d->Cin, d->N), channel_dim(d->N),
+         cols, channel_dim(d->N), column_dim(d->Cout, d->N));
+  g.K = d->Cin;
+  g.bias = bias;
+  g.residual = residual;
+  g.z = {z, 1};
+  g.d = {y, y_type == MQV_BF16};
+  g.act = d->act;
+  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_type, const void* z, void* gz,
+                            float* gbias, void* ws, size_t ws_bytes, void* stream) {
+  mqv_status st = check_lin(d);
+  if (st || (st = check_type(gy_type, "gy"))) return st;
+  const int64_t cols = d->P * d->N, n = cols * d->Cout;
+  if (!gz && !gbias) return fail(MQV_ERR_INVALID_ARG, "gz and gbias: one at least");
+  const int64_t need = gbias ? lin_ws(d, MQV_OP_ACT_GRAD) : 0;
+  if ((st = check_workspace(ws, ws_bytes, need))) return st;
+  const bool act = d->act != MQV_ACT_NONE;
+  if ((st = check_buffers({{"gy", gy, n * type_size(gy_type), false, true},
+                           {"z", act ? z : nullptr, n * 2, false, act},
+                           {"gz", gz, n * 2, true, false},
+                           {"gbias", gbias, d->Cout * 4, true, false},
+                           {"ws", ws, need, true, false}},
+                          "gz", "gy")))
+    return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const ActGradPlan pl = plan_act_grad(d);
+  ActGradArgs a = {};
+  a.gy = {gy, gy_type == MQV_BF16};
+  a.z = act ? z : nullptr;
+  a.gz = {gz, 1};
+  a.part = gbias ? static_cast<float*>(ws) : nullptr;
+  a.P = d->P;
+  a.N = d->N;
+  a.C = (int)d->Cout;
+  a.act = d->act;
+  a.lanes = pl.lanes;
+  a.rows = pl.rows;
+  a.tiles = pl.tiles;
+  const dim3 grid(pl.gx, pl.gy);
+  if (cols > 0) {
+    if (d->N == 1) {
+      if (pl.v == 8)
+        act_grad_row_kernel<8><<<grid, 256, 0, s>>>(a);
+      else
+        act_grad_row_kernel<1><<<grid, 256, 0, s>>>(a);
+    } else {
+      if (pl.v == 8)
+        act_grad_tile_kernel<8><<<grid, 256, 0, s>>>(a);
+      else if (pl.v == 4)
+        act_grad_tile_kernel<4><<<grid, 256, 0, s>>>(a);
+      else
+        act_grad_tile_kernel<1><<<grid, 256, 0, s>>>(a);
+    }
+  }
+  if (gbias) launch_column_sum(a.part, cols > 0 ? pl.gy : 0, d->Cout, 1, gbias, nullptr, s);
+  return launched("activation gradient launch");
+}
+
+mqv_status mqv_lin_dgrad(const mqv_lin_desc* d, const void* w, const void* gz, void* gx, int32_t gx_type, void* ws,
+                         size_t ws_bytes, void* stream) {
+  mqv_status st = check_lin(d);
+  if (st || (st = check_type(gx_type, "gx"))) return st;
+  const int64_t cols = d->P * d->N, need = lin_ws(d, MQV_OP_DGRAD);
+  if ((st = check_workspace(ws, ws_bytes, need))) return st;
+  if ((st = check_buffers({{"w", w, d->Cout * d->Cin * 2, false, true},
+                           {"gz", gz, cols * d->Cout * 2, false, true},
+                           {"gx", gx, cols * d->Cin * type_size(gx_type), true, true},
+                           {"ws", ws, need, true, false}})))
+    return st;
+  GemmArgs g = {};
+  orient(&g, d->N == 1, w, channel_dim(1), channel_dim(d->Cin), d->Cin, gz, column_dim(d->Cout, d->N),
+         channel_dim(d->N), cols, channel_dim(d->N), column_dim(d->Cin, d->N));
+  g.K = d->Cout;
+  g.d = {gx, gx_type == MQV_BF16};
+  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, float* gw, void* ws, size_t ws_bytes,
+                         void* stream) {
+  mqv_status st = check_lin(d);
+  if (st) return st;
+  const int64_t cols = d->P * d->N, need = lin_ws(d, MQV_OP_WGRAD);
+  if ((st = check_workspace(ws, ws_bytes, need))) return st;
+  if ((st = check_buffers({{"gz", gz, cols * d->Cout * 2, false, true},
+                           {"x", x, cols * d->Cin * 2, false, true},
+                           {"gw", gw, d->Cout * d->Cin * 4, true, true},
+                           {"ws", ws, need, true, false}})))
+    return st;
+  GemmArgs g = {};
+  g.a = static_cast<const uint16_t*>(gz);
+  g.a_row = channel_dim(d->N);
+  g.a_k = column_dim(d->Cout, d->N);
+  g.b = static_cast<const uint16_t*>(x);
+  g.b_col = channel_dim(d->N);
+  g.b_k = column_dim(d->Cin, d->N);
+  g.M = d->Cout;
+  g.N = d->Cin;
+  g.K = cols;
+  g.d = {gw, 0};
+  g.d_row = channel_dim(d->Cin);
+  g.d_col = channel_dim(1);
+  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,40 @@
+"""Shapes and inputs of the layer norm and linear layer tests."""
+import numpy as np
+import torch
+
+# (P, C, N).  Token rows: one element, one token, widths that are no multiple
+# of a vector, the widths at which the vectors per thread change, the widest.
+LN_ROWS = [(1, 1, 1), (1, 8, 1), (3, 7, 1), (1, 1024, 1), (5, 1023, 1), (2, 2048, 1), (3, 2056, 1), (2, 4099, 1),
+           (300, 64, 1), (700, 136, 1), (2, 16384, 1), (1, 16383, 1), (1300, 264, 1)]
+# Batch columns: one channel, odd batches, whole and ragged tiles of 64 batch
+# items, more channels than the widest tile takes, a large batch.
+LN_TILES = [(1, 1, 2), (3, 5, 3), (7, 64, 16), (4, 128, 64), (2, 512, 64), (2, 2048, 8), (1, 4096, 4), (1, 16384, 4),
+            (1, 5000, 3), (5, 33, 84), (2, 16, 200), (3, 20, 12), (1, 3, 10240), (600, 16, 4), (800, 24, 32)]
+
+# (P, Cin, Cout, N)
+LIN_TOKENS = [(1, 1, 1, 1), (1, 64, 64, 1), (1, 1000, 1003, 1), (2, 2048, 96, 1), (3, 5, 7, 1), (8, 1000, 1003, 1),
+              (9, 128, 64, 1), (17, 8, 8, 1), (64, 256, 512, 1), (130, 72, 136, 1), (129, 257, 255, 1),
+              (513, 96, 200, 1), (300, 1024, 264, 1), (1, 4096, 512, 1), (1025, 128, 640, 1), (33, 520, 1024, 1)]
+LIN_PIXELS = [(1, 3, 5, 2), (7, 16, 8, 4), (49, 64, 64, 16), (5, 33, 40, 12), (4, 128, 256, 64), (3, 64, 100, 84),
+              (10, 24, 24, 8), (3, 40, 48, 32), (2, 16, 16, 200), (6, 65, 63, 16), (1, 128, 128, 96), (30, 64, 128, 24),
+              (1, 200, 72, 7), (100, 16, 24, 16), (2, 136, 320, 128)]
+
+
+def shape_id(s):
+    return "x".join(map(str, s))
+
+
+def bf16(a):
+    """a rounded to bfloat16, as fp64."""
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(torch.bfloat16).double().numpy()
+
+
+def stored(a, kind):
+    """a as the type `kind` holds it, fp64."""
+    return bf16(a) if kind == "bf16" else np.ascontiguousarray(a, np.float32).astype(np.float64)
+
+
+def activations(rng, shape):
+    """Unit noise over channel offsets, a few channels much larger than the others."""
+    x = rng.standard_normal(shape) * np.where(rng.random((shape[1], 1)) < 0.05, 20.0, 1.0)
+    return x + rng.standard_normal((shape[1], 1)) * 3.0

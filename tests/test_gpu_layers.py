@@ -1,0 +1,400 @@
+"""GPU parity of the layer norm and the linear layer against their fp64
+definitions, every output within the oracle's error bound, the same bits on a
+second run; streams, graphs, in-place forms, special values and refusals."""
+import numpy as np
+import pytest
+import torch
+
+import microscaling_quantized_convolution_b200 as mqv
+from oracle import layers_oracle as L
+from tests.layers_cases import LIN_PIXELS, LIN_TOKENS, LN_ROWS, LN_TILES, activations, shape_id, stored
+
+pytestmark = pytest.mark.gpu
+
+KIND = {torch.float32: "f32", torch.bfloat16: "bf16"}
+F32, BF16 = torch.float32, torch.bfloat16
+EPS = float(np.float32(1e-5))          # the descriptor holds fp32
+
+
+def dev(a, dtype=F32):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda()
+
+
+def check(got, ref, what):
+    value, err = ref
+    lim = L.rounding(value, err, KIND[got.dtype])
+    g = got.double().cpu().numpy().reshape(value.shape)
+    off = np.abs(g - value)
+    bad = ~(off <= lim)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}, "
+                           f"worst {np.max(off / lim):.3g} of the bound")
+
+
+def poison(shape, dtype):
+    return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+# -------------------------------------------------------------- layer norm
+
+TYPES = [(F32, F32), (F32, BF16), (BF16, BF16), (BF16, F32)]
+
+
+def ln_inputs(shape, seed=0):
+    rng = np.random.default_rng(sum(shape) + seed)
+    P, C, N = shape
+    return (activations(rng, shape), rng.standard_normal(C) * 0.3 + 1, rng.standard_normal(C) * 0.3,
+            rng.standard_normal(shape) * 1e-2)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES, ids=["f32-f32", "f32-bf16", "bf16-bf16", "bf16-f32"])
+@pytest.mark.parametrize("shape", LN_ROWS + LN_TILES, ids=shape_id)
+def test_layer_norm(shape, xt, yt):
+    P, C, N = shape
+    x, gamma, beta, gy = ln_inputs(shape)
+    x, gy = stored(x, KIND[xt]), stored(gy, KIND[yt])
+    gamma, beta = stored(gamma, "f32"), stored(beta, "f32")
+    d = mqv.ln_desc(P, C, N)
+    xd, gyd, gd, bd = dev(x, xt), dev(gy, yt), dev(gamma), dev(beta)
+    y, mean, rstd = mqv.ln_fwd(d, xd, gd, bd, y=poison(shape, yt), mean=poison((P, N), F32), rstd=poison((P, N), F32))
+    ref = L.ln_fwd(x, gamma, beta, EPS)
+    for got, name in ((y, "y"), (mean, "mean"), (rstd, "rstd")):
+        check(got, ref[name], name)
+    for gxt in (F32, BF16):
+        gx, gg, gb = mqv.ln_bwd(d, gyd, xd, mean, rstd, gd, gx=poison(shape, gxt), ggamma=poison((C,), F32),
+                                gbeta=poison((C,), F32))
+        bref = L.ln_bwd(gy, x, mean.double().cpu().numpy(), rstd.double().cpu().numpy(), gamma)
+        for got, name in ((gx, "gx"), (gg, "ggamma"), (gb, "gbeta")):
+            check(got, bref[name], name)
+    y2, mean2, rstd2 = mqv.ln_fwd(d, xd, gd, bd, y_dtype=yt)
+    gx2, gg2, gb2 = mqv.ln_bwd(d, gyd, xd, mean2, rstd2, gd, gx_dtype=gxt)
+    for a, b in ((y, y2), (mean, mean2), (rstd, rstd2), (gx, gx2), (gg, gg2), (gb, gb2)):
+        assert torch.equal(a, b.view(a.shape))
+
+
+@pytest.mark.parametrize("shape", [(9, 264, 1), (9, 33, 1), (5, 24, 16), (3, 20, 12)], ids=shape_id)
+def test_layer_norm_without_parameters_or_statistics(shape):
+    x, _, _, gy = ln_inputs(shape)
+    x, gy = stored(x, "f32"), stored(gy, "f32")
+    d = mqv.ln_desc(*shape)
+    y, mean, rstd = mqv.ln_fwd(d, dev(x), stats=False)
+    assert mean is None and rstd is None
+    ref = L.ln_fwd(x, None, None, EPS)
+    check(y, ref["y"], "y")
+    y1, _, _ = mqv.ln_fwd(d, dev(x), gamma=dev(np.full(shape[1], 2.0)), stats=False)       # gamma without beta
+    check(y1, L.ln_fwd(x, np.full(shape[1], 2.0), None, EPS)["y"], "y")
+    _, mean, rstd = mqv.ln_fwd(d, dev(x))
+    gx, gg, gb = mqv.ln_bwd(d, dev(gy), dev(x), mean, rstd, param_grads=False)
+    assert gg is None and gb is None
+    bref = L.ln_bwd(gy, x, mean.double().cpu().numpy(), rstd.double().cpu().numpy(), None)
+    check(gx, bref["gx"], "gx")
+    _, gg, gb = mqv.ln_bwd(d, dev(gy), dev(x), mean, rstd)
+    check(gg, bref["ggamma"], "ggamma")
+    check(gb, bref["gbeta"], "gbeta")
+
+
+@pytest.mark.parametrize("shape", [(4, 512, 1), (4, 100, 1), (3, 64, 16)], ids=shape_id)
+def test_layer_norm_in_place(shape):
+    x, gamma, beta, gy = ln_inputs(shape)
+    d = mqv.ln_desc(*shape)
+    xd, gyd = dev(x), dev(gy)
+    y, mean, rstd = mqv.ln_fwd(d, xd, dev(gamma), dev(beta))
+    gx, _, _ = mqv.ln_bwd(d, gyd, xd, mean, rstd, dev(gamma))
+    g2 = gyd.clone()
+    assert torch.equal(mqv.ln_bwd(d, g2, xd, mean, rstd, dev(gamma), gx=g2)[0], gx)
+    x2 = xd.clone()
+    assert torch.equal(mqv.ln_fwd(d, x2, dev(gamma), dev(beta), y=x2)[0], y)
+
+
+@pytest.mark.parametrize("shape", [(6, 320, 1), (6, 33, 1), (6, 48, 16)], ids=shape_id)
+def test_layer_norm_special_columns(shape):
+    """A NaN or infinity spoils its own column only; a constant column gives
+    beta; a large common offset keeps its precision."""
+    P, C, N = shape
+    x, gamma, beta, _ = ln_inputs(shape)
+    x = stored(x, "f32")
+    x[0, 3, 0] = np.nan
+    x[1, C - 1, 0] = np.inf
+    x[2, 0, 0] = -np.inf
+    x[3, :, 0] = 7.25
+    x[4, :, 0] = stored(4096.0 + x[4, :, 0], "f32")
+    d = mqv.ln_desc(*shape)
+    y, mean, rstd = mqv.ln_fwd(d, dev(x), dev(gamma), dev(beta))
+    bad = torch.isnan(y)
+    assert bad[:3, :, 0].all() and bad.sum() == 3 * C
+    ref = L.ln_fwd(x[3:], stored(gamma, "f32"), stored(beta, "f32"), EPS)
+    check(y[3:], ref["y"], "y")
+    assert torch.equal(y[3, :, 0], dev(beta))
+    if N > 1:
+        ref = L.ln_fwd(x[:, :, 1:], stored(gamma, "f32"), stored(beta, "f32"), EPS)
+        check(y[:, :, 1:].contiguous(), ref["y"], "y")
+
+
+def test_layer_norm_of_nothing():
+    for N in (1, 16):
+        d = mqv.ln_desc(0, 64, N)
+        x = torch.empty((0, 64, N), device="cuda")
+        y, mean, rstd = mqv.ln_fwd(d, x)
+        gx, gg, gb = mqv.ln_bwd(d, x, x, mean, rstd, ggamma=poison((64,), F32), gbeta=poison((64,), F32))
+        assert y.shape == gx.shape == x.shape and not gg.any() and not gb.any()
+
+
+# ------------------------------------------------------------ linear layer
+
+def lin_inputs(shape, seed=0):
+    P, Cin, Cout, N = shape
+    rng = np.random.default_rng(sum(shape) + seed)
+    return (stored(rng.standard_normal((Cout, Cin)) * (2.0 / Cin) ** 0.5, "bf16"),
+            stored(activations(rng, (P, Cin, N)), "bf16"), stored(rng.standard_normal(Cout) * 0.1, "f32"),
+            rng.standard_normal((P, Cout, N)), rng.standard_normal((P, Cout, N)) * 1e-2)
+
+
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS, ids=shape_id)
+def test_linear_layer(shape):
+    P, Cin, Cout, N = shape
+    w, x, bias, res, gy = lin_inputs(shape)
+    out = (P, Cout, N)
+    wd, xd, bd = dev(w, BF16), dev(x, BF16), dev(bias)
+    for act, yt, use_bias, use_res in (("none", F32, False, False), ("gelu", BF16, True, True),
+                                       ("silu", F32, True, False), ("relu", BF16, False, True)):
+        r = stored(res, KIND[yt])
+        d = mqv.lin_desc(P, Cin, Cout, N, act)
+        args = dict(bias=bd if use_bias else None, residual=dev(r, yt) if use_res else None)
+        y, z = mqv.lin_fwd(d, wd, xd, **args, y=poison(out, yt), z=poison(out, BF16))
+        ref = L.lin_fwd(w, x, bias if use_bias else None, r if use_res else None, act)
+        check(y, ref["y"], f"y ({act})")
+        check(z, ref["z"], f"z ({act})")
+        y2, none = mqv.lin_fwd(d, wd, xd, **args, y_dtype=yt)
+        assert none is None and torch.equal(y, y2)
+    gz = stored(gy, "bf16")
+    gzd = dev(gz, BF16)
+    for gxt in (F32, BF16):
+        gx = mqv.lin_dgrad(d, wd, gzd, gx=poison((P, Cin, N), gxt))
+        check(gx, L.lin_dgrad(w, gz)["gx"], "gx")
+    gw = mqv.lin_wgrad(d, gzd, xd, gw=poison((Cout, Cin), F32))
+    check(gw, L.lin_wgrad(gz, x)["gw"], "gw")
+    assert torch.equal(gx, mqv.lin_dgrad(d, wd, gzd)) and torch.equal(gw, mqv.lin_wgrad(d, gzd, xd))
+    assert mqv.device_errors() == 0
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 9, 1), (5, 1003, 1), (300, 64, 1), (2100, 520, 1), (3, 5, 2),
+                                   (49, 64, 16), (40, 33, 12), (600, 24, 64), (5, 3, 84), (2, 2, 5000), (3, 7, 2056)],
+                         ids=shape_id)
+def test_activation_gradient(shape, act):
+    P, C, N = shape
+    rng = np.random.default_rng(sum(shape))
+    z = stored(rng.standard_normal(shape) * 3, "bf16")
+    d = mqv.lin_desc(P, 8, C, N, act)
+    for gt in (F32, BF16):
+        gy = stored(rng.standard_normal(shape) * 1e-2, KIND[gt])
+        gz, gb = mqv.lin_act_grad(d, dev(gy, gt), dev(z, BF16), gz=poison(shape, BF16), gbias=poison((C,), F32))
+        ref = L.lin_act_grad(gy, z, act)
+        check(gz, ref["gz"], "gz")
+        check(gb, ref["gbias"], "gbias")
+        gz2, gb2 = mqv.lin_act_grad(d, dev(gy, gt), dev(z, BF16))
+        assert torch.equal(gz, gz2) and torch.equal(gb, gb2)
+        gz3, none = mqv.lin_act_grad(d, dev(gy, gt), dev(z, BF16), bias_grad=False)
+        assert none is None and torch.equal(gz, gz3)
+    g = dev(gy, BF16)
+    assert torch.equal(mqv.lin_act_grad(d, g, dev(z, BF16), gz=g)[0], gz)          # in place
+
+
+def test_activation_extremes():
+    """Far arguments: the activations and slopes reach their limits without
+    a NaN, and a NaN passes through."""
+    z = torch.tensor([0.0, -0.0, 80.0, -80.0, 1e30, -1e30, float("nan")], device="cuda").to(BF16).view(7, 1, 1)
+    one = torch.ones((1, 1), dtype=BF16, device="cuda")
+    gy = torch.ones((7, 1, 1), device="cuda")
+    for act in ("relu", "gelu", "silu"):
+        d = mqv.lin_desc(7, 1, 1, 1, act)
+        y, _ = mqv.lin_fwd(d, one, z, y_dtype=F32)
+        s, _ = mqv.lin_act_grad(d, gy, z)
+        zf = z.double().cpu().numpy()[:6]
+        check(y[:6], (L.act_value(zf, act), 24 * L.U * np.abs(zf) * (zf > -60)), act)
+        check(s[:6], (L.act_slope(zf, act), np.full_like(zf, 16 * L.U)), act)
+        assert torch.isnan(y[6, 0, 0]) and (act == "relu" or torch.isnan(s[6, 0, 0]))
+
+
+def test_linear_layer_of_nothing():
+    for N in (1, 16):
+        d = mqv.lin_desc(0, 24, 40, N, "gelu")
+        w = torch.ones((40, 24), dtype=BF16, device="cuda")
+        x = torch.empty((0, 24, N), dtype=BF16, device="cuda")
+        y, z = mqv.lin_fwd(d, w, x, save_z=True)
+        gz, gb = mqv.lin_act_grad(d, y, z, gbias=poison((40,), F32))
+        gx, gw = mqv.lin_dgrad(d, w, gz), mqv.lin_wgrad(d, gz, x, gw=poison((40, 24), F32))
+        assert y.shape == (0, 40, N) and gx.shape == (0, 24, N) and not gb.any() and not gw.any()
+
+
+def test_linear_layer_residual_in_place():
+    for shape in ((70, 128, 136, 1), (5, 64, 48, 16), (1, 64, 200, 1)):
+        w, x, bias, res, _ = lin_inputs(shape)
+        P, Cin, Cout, N = shape
+        d = mqv.lin_desc(*shape)
+        for t in (F32, BF16):
+            r = dev(res, t)
+            y, _ = mqv.lin_fwd(d, dev(w, BF16), dev(x, BF16), dev(bias), residual=r)
+            assert y.dtype == t
+            assert torch.equal(mqv.lin_fwd(d, dev(w, BF16), dev(x, BF16), dev(bias), residual=r, y=r)[0], y)
+
+
+def test_infinite_inputs_stay_in_their_outputs():
+    """An infinity or NaN in one token reaches that token's outputs only."""
+    for shape in ((70, 128, 136, 1), (3, 64, 48, 16), (4, 64, 64, 1)):
+        P, Cin, Cout, N = shape
+        w, x, bias, _, _ = lin_inputs(shape)
+        d = mqv.lin_desc(*shape)
+        y, _ = mqv.lin_fwd(d, dev(w, BF16), dev(x, BF16), dev(bias))
+        x[1, 5, 0], x[2, 0, 0] = np.nan, np.inf
+        b, _ = mqv.lin_fwd(d, dev(w, BF16), dev(x, BF16), dev(bias))
+        fine = torch.isfinite(b)
+        assert not fine[1, :, 0].any() and not fine[2, :, 0].any() and (~fine).sum() == 2 * Cout
+        assert torch.equal(b[fine], y[fine])
+
+
+# ----------------------------------- streams, graphs, workspaces, refusals
+
+def _block(d1, d2, ln, t, x, **kw):
+    """Pre-norm MLP with residual, forward and backward, every pass of it."""
+    h, mean, rstd = mqv.ln_fwd(ln, x, t["gamma"], t["beta"], y_dtype=BF16, **kw)
+    a, z = mqv.lin_fwd(d1, t["w1"], h, bias=t["b1"], save_z=True, **kw)
+    y, _ = mqv.lin_fwd(d2, t["w2"], a, bias=t["b2"], residual=x, **kw)
+    gy = t["gy"]
+    g2, gb2 = mqv.lin_act_grad(d2, gy, **kw)
+    ga, gw2 = mqv.lin_dgrad(d2, t["w2"], g2, **kw), mqv.lin_wgrad(d2, g2, a, **kw)
+    g1, gb1 = mqv.lin_act_grad(d1, ga, z, **kw)
+    gh, gw1 = mqv.lin_dgrad(d1, t["w1"], g1, **kw), mqv.lin_wgrad(d1, g1, h, **kw)
+    gx, gg, gb = mqv.ln_bwd(ln, gh, x, mean, rstd, t["gamma"], **kw)
+    return {"y": y, "gb2": gb2, "gw2": gw2, "gb1": gb1, "gw1": gw1, "gx": gx, "ggamma": gg, "gbeta": gb}
+
+
+def _block_inputs(P, C, H, N, seed=0):
+    rng = np.random.default_rng(seed)
+    t = {"w1": dev(rng.standard_normal((H, C)) * (2 / C) ** 0.5, BF16), "b1": dev(rng.standard_normal(H) * 0.1),
+         "w2": dev(rng.standard_normal((C, H)) * (1 / H) ** 0.5, BF16), "b2": dev(rng.standard_normal(C) * 0.1),
+         "gamma": dev(rng.standard_normal(C) * 0.2 + 1), "beta": dev(rng.standard_normal(C) * 0.2),
+         "gy": dev(rng.standard_normal((P, C, N)) * 1e-2, BF16)}
+    x = dev(rng.standard_normal((P, C, N)), BF16)
+    return t, x, mqv.lin_desc(P, C, H, N, "gelu"), mqv.lin_desc(P, H, C, N), mqv.ln_desc(P, C, N)
+
+
+def _block_fp64(t, x):
+    p = {k: v.double().requires_grad_() for k, v in t.items() if k != "gy"}
+    xx = x.double()
+    xx.requires_grad_()
+    m = xx.mean(1, keepdim=True)
+    v = (xx - m).square().mean(1, keepdim=True)
+    h = (xx - m) / (v + 1e-5).sqrt() * p["gamma"][:, None] + p["beta"][:, None]
+    z = torch.einsum("oi,pin->pon", p["w1"], h) + p["b1"][:, None]
+    y = torch.einsum("oi,pin->pon", p["w2"], torch.nn.functional.gelu(z)) + p["b2"][:, None]
+    (y * t["gy"].double()).sum().backward()
+    return {"y": y.detach() + x.double(), "gb2": p["b2"].grad, "gw2": p["w2"].grad, "gb1": p["b1"].grad,
+            "gw1": p["w1"].grad, "gx": xx.grad, "ggamma": p["gamma"].grad, "gbeta": p["beta"].grad}
+
+
+BLOCKS = [(200, 96, 264, 1), (1, 64, 128, 1), (37, 33, 70, 1), (25, 64, 128, 16), (9, 24, 56, 12)]
+
+
+@pytest.mark.parametrize("shape", BLOCKS, ids=shape_id)
+def test_block_of_norm_and_linear_layers(shape):
+    """The passes chained as a block uses them.  bfloat16 intermediates (h, a,
+    z, ga, g1, gh: at most six roundings of 2^-8 on any path, each entering a
+    sum of random signs) leave the outputs within 6·2^-8 of the fp64 block in
+    the 2-norm."""
+    t, x, d1, d2, ln = _block_inputs(*shape)
+    got, ref = _block(d1, d2, ln, t, x), _block_fp64(t, x)
+    for k, v in got.items():
+        off = (v.double() - ref[k]).norm() / ref[k].norm()
+        assert off < 6 * 2 ** -8, f"{k}: {off:.3g}"
+    assert mqv.device_errors() == 0
+
+
+@pytest.mark.parametrize("shape", BLOCKS, ids=shape_id)
+def test_block_on_another_stream_and_in_a_graph(shape):
+    t, x, d1, d2, ln = _block_inputs(*shape)
+    want = {k: v.clone() for k, v in _block(d1, d2, ln, t, x).items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = _block(d1, d2, ln, t, x, stream=s)
+    s.synchronize()
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    # two graphs, replayed side by side on two streams, each several times
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = _block(d1, d2, ln, t, x)
+        graphs.append((g, out, torch.cuda.Stream()))
+    for g, out, st in graphs:
+        for v in out.values():
+            v.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, out, st in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for g, out, st in graphs:
+        for k in want:
+            assert torch.equal(out[k], want[k]), k
+    # new inputs reach a replay
+    x.mul_(-1.5)
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    fresh = _block(d1, d2, ln, t, x)
+    for k in want:
+        assert torch.equal(graphs[0][1][k], fresh[k]), k
+
+
+def test_given_workspaces_and_ragged_pointers():
+    shape = (90, 72, 136, 1)
+    w, x, bias, _, gy = lin_inputs(shape)
+    d = mqv.lin_desc(*shape, "silu")
+    wd, xd, gd = dev(w, BF16), dev(x, BF16), dev(gy, BF16)
+    for op, call in ((mqv.OP_FWD, lambda ws: mqv.lin_fwd(d, wd, xd, ws=ws)[0]),
+                     (mqv.OP_DGRAD, lambda ws: mqv.lin_dgrad(d, wd, gd, ws=ws)),
+                     (mqv.OP_WGRAD, lambda ws: mqv.lin_wgrad(d, gd, xd, ws=ws)),
+                     (mqv.OP_ACT_GRAD, lambda ws: mqv.lin_act_grad(d, gd, gd, ws=ws)[1])):
+        need = mqv.lin_workspace_bytes(d, op)
+        want = call(None)
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(call(ws[:need]), want)
+        assert (ws[need:] == 255).all()
+        if need:
+            with pytest.raises(mqv.MqvError):
+                call(ws[:need - 1])
+            with pytest.raises(mqv.MqvError):
+                call(ws[8:])
+    big = torch.zeros(90 * 72 + 4, dtype=BF16, device="cuda")
+    with pytest.raises(mqv.MqvError):                              # 8 bytes off a 16-byte boundary
+        mqv.lin_fwd(d, wd, big[4:])
+
+
+def test_binding_refusals():
+    d, ln = mqv.lin_desc(4, 16, 24, 1, "gelu"), mqv.ln_desc(4, 16)
+    w = torch.zeros((24, 16), dtype=BF16, device="cuda")
+    x, y = torch.zeros((4, 16), dtype=BF16, device="cuda"), torch.zeros((4, 24), dtype=BF16, device="cuda")
+    s, f = torch.zeros(4, device="cuda"), torch.zeros((4, 16), device="cuda")
+    short = torch.zeros(5, dtype=BF16, device="cuda")
+    bad = [
+        lambda: mqv.lin_fwd(d, w, short), lambda: mqv.lin_fwd(d, short, x), lambda: mqv.lin_fwd(d, w, f),
+        lambda: mqv.lin_fwd(d, w, x.t()), lambda: mqv.lin_fwd(d, w, x, bias=s), lambda: mqv.lin_fwd(d, w, x, bias=y),
+        lambda: mqv.lin_fwd(d, w, x, residual=y, y_dtype=F32), lambda: mqv.lin_fwd(d, w, x, y=short),
+        lambda: mqv.lin_fwd(d, w, x, z=short), lambda: mqv.lin_fwd(d, w, x, y_dtype=torch.float16),
+        lambda: mqv.lin_fwd(d, w.cpu(), x), lambda: mqv.lin_fwd(d, w, x, y=y, y_dtype=F32),
+        lambda: mqv.lin_act_grad(d, y), lambda: mqv.lin_act_grad(d, y, short), lambda: mqv.lin_act_grad(d, short, y),
+        lambda: mqv.lin_act_grad(d, y, y, gbias=s), lambda: mqv.lin_dgrad(d, w, short),
+        lambda: mqv.lin_dgrad(d, w, y, gx=short), lambda: mqv.lin_wgrad(d, short, x), lambda: mqv.lin_wgrad(d, y, short),
+        lambda: mqv.lin_wgrad(d, y, x, gw=w), lambda: mqv.ln_fwd(ln, short), lambda: mqv.ln_fwd(ln, x.half()),
+        lambda: mqv.ln_fwd(ln, x, gamma=s), lambda: mqv.ln_fwd(ln, x, mean=short),
+        lambda: mqv.ln_bwd(ln, x, x, s, short), lambda: mqv.ln_bwd(ln, short, x, s, s),
+        lambda: mqv.ln_bwd(ln, x, x, s, s, ws=torch.zeros(4096)),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    with pytest.raises(mqv.MqvError):                              # two outputs in one buffer
+        mqv.ln_fwd(ln, x, mean=s, rstd=s)
+    assert mqv.device_errors() == 0
