@@ -1,6 +1,7 @@
 // C ABI of the BF16 layers around the quantized convolutions (declared in
 // include/mqv.h): layer norm and the linear layer.  Argument validation and
 // launch geometry; the arithmetic is in mqv_norm.cuh and mqv_linear.cuh.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -8,6 +9,7 @@
 #include <initializer_list>
 
 #include "mqv.h"
+#include "mqv_gemm.cuh"
 #include "mqv_host.h"
 #include "mqv_linear.cuh"
 #include "mqv_norm.cuh"
@@ -18,7 +20,7 @@ using namespace mqv;
 
 constexpr int kSms = 148;
 constexpr int64_t kMaxChannels = 16384;             // layer norm: a position's channels in one block's registers
-constexpr int64_t kMaxElements = int64_t{1} << 40;
+constexpr int64_t kMaxElements = int64_t{1} << 38;
 constexpr int64_t kMaxColumns = (int64_t{1} << 31) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -230,34 +232,223 @@ ActGradPlan plan_act_grad(const mqv_lin_desc* d) {
   return pl;
 }
 
-int64_t lin_ws(const mqv_lin_desc* d, int op) {
-  if (op == MQV_OP_ACT_GRAD) return align256((int64_t)plan_act_grad(d).gy * d->Cout * 4);
-  return 0;
+// ---- products on the tensor cores
+
+// A [pos][mid][inner] view of an operand, rows of `inner` elements.
+struct GemmView {
+  int64_t pos, mid, inner;
+  bool mn_major;               // the tile's rows lie along inner, else K does
+  int64_t pitch() const { return ceil_div(inner, 8) * 8; }
+  bool copied() const { return inner % 8 != 0; }
+  int64_t copy_bytes() const { return copied() ? align256(pos * mid * pitch() * 2) : 0; }
+};
+
+// One pass as D = A·B^T over the views; D's columns are contiguous.
+struct GemmPlan {
+  GemmView a, b;
+  GemmOperand oa, ob;
+  int64_t M;
+  int bn;
+  GemmTcArgs args;
+  int64_t out_elems, part_bytes, ws_bytes;
+};
+
+// The chunk size of an inner extent: the largest whose padding stays within
+// an eighth, else the one with the least padding.
+int chunk_of(int64_t inner) {
+  int best = 16;
+  for (int c : {64, 32, 16}) {
+    if (ceil_div(inner, c) * c * 8 <= inner * 9) return c;
+    if (ceil_div(inner, c) * c < ceil_div(inner, best) * best) best = c;
+  }
+  return best;
 }
 
-Dim channel_dim(int64_t N) { return {int64_t{1} << 62, 0, N}; }
-Dim column_dim(int64_t C, int64_t N) { return {N, C * N, 1}; }
+GemmOperand operand_of(const GemmView& v, int rows, bool batch) {
+  GemmOperand o;
+  o.chunk = batch ? chunk_of(v.inner) : 64;
+  o.per_pos = (int)ceil_div(v.inner, o.chunk);
+  o.mn_major = v.mn_major;
+  o.box = batch && o.per_pos == 1 ? (v.mn_major ? rows : kGemmBK) / o.chunk : 1;
+  return o;
+}
 
-mqv_status launch_gemm(const GemmArgs& g, cudaStream_t st) {
-  const int64_t blocks = ceil_div(g.M, 64) * ceil_div(g.N, 64);
-  if (blocks == 0) return ok();
-  gemm_simple_kernel<<<(unsigned)blocks, 256, 0, st>>>(g);
+void plan_gemm(const mqv_lin_desc* d, int op, GemmPlan* pl) {
+  const bool tokens = d->N == 1;
+  // a [P][C][N] tensor: rows of channels for tokens, of batch items otherwise
+  auto tensor = [&](int64_t C, bool mn) {
+    return tokens ? GemmView{1, d->P, C, mn} : GemmView{d->P, C, d->N, mn};
+  };
+  GemmTcArgs& g = pl->args;
+  g = {};
+  int64_t kdim = 0;            // channels contracted over; 0: the columns
+  int64_t cols;
+  bool batch_a = false, batch_b = false;
+  if (op == MQV_OP_WGRAD) {
+    pl->a = tensor(d->Cout, tokens);
+    pl->b = tensor(d->Cin, tokens);
+    batch_a = batch_b = !tokens;
+    pl->M = d->Cout;
+    cols = d->Cin;
+  } else {
+    const int64_t out = op == MQV_OP_FWD ? d->Cout : d->Cin;
+    kdim = op == MQV_OP_FWD ? d->Cin : d->Cout;
+    const GemmView w{1, d->Cout, d->Cin, op == MQV_OP_DGRAD};
+    if (tokens) {
+      pl->a = tensor(kdim, false);
+      pl->b = w;
+      pl->M = d->P;
+      cols = out;
+    } else {
+      pl->a = w;
+      pl->b = tensor(kdim, true);
+      batch_b = true;
+      pl->M = out;
+      cols = 0;
+    }
+  }
+  const bool col_batch = op != MQV_OP_WGRAD && !tokens;
+  g.M = pl->M;
+  g.col_chunk = col_batch ? chunk_of(d->N) : 64;
+  g.col_inner = col_batch ? d->N : cols;
+  g.col_pos = col_batch ? d->P : 1;
+  g.col_per_pos = (int)ceil_div(g.col_inner, g.col_chunk);
+  g.row_stride = g.col_inner;
+  g.pos = col_batch ? pl->M * d->N : 0;
+  g.e.vec4 = g.col_inner % 4 == 0;
+  g.e.bias_on_row = col_batch;
+  pl->out_elems = pl->M * g.col_inner * g.col_pos;
+  const int64_t vcols = g.col_pos * g.col_per_pos * g.col_chunk;
+  pl->bn = vcols <= 64 ? 64 : vcols <= 128 ? 128 : 256;
+  g.tiles_m = (int)ceil_div(pl->M, kGemmBM);
+  // narrower tiles while the wide ones leave half of the SMs without work
+  while (pl->bn > 64 && g.tiles_m * ceil_div(vcols, pl->bn) * 2 <= kSms) pl->bn /= 2;
+  g.tiles_n = (int)ceil_div(vcols, pl->bn);
+  pl->oa = operand_of(pl->a, kGemmBM, batch_a);
+  pl->ob = operand_of(pl->b, pl->bn, batch_b);
+  g.a = pl->oa;
+  g.b = pl->ob;
+  g.kblocks = (int)(kdim ? ceil_div(kdim, kGemmBK)
+                         : batch_a ? ceil_div(d->P * pl->oa.per_pos, kGemmBK / pl->oa.chunk) : ceil_div(d->P, kGemmBK));
+  // split K while tiles leave SMs idle and a split keeps four K blocks
+  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
+  g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(tiles, 1), g.kblocks / 4));
+  g.part_stride = ceil_div(pl->out_elems, 4) * 4;
+  pl->part_bytes = g.splits > 1 ? align256(g.splits * g.part_stride * 4) : 0;
+  pl->ws_bytes = pl->part_bytes + pl->a.copy_bytes() + pl->b.copy_bytes();
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn tensor_map_encoder() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+mqv_status encode(CUtensorMap* map, const void* p, const GemmView& v, const GemmOperand& o, int rows) {
+  const EncodeFn fn = tensor_map_encoder();
+  if (!fn) return fail(MQV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from this driver");
+  const cuuint64_t dims[3] = {(cuuint64_t)v.inner, (cuuint64_t)v.mid, (cuuint64_t)v.pos};
+  const cuuint64_t strides[2] = {(cuuint64_t)v.pitch() * 2, (cuuint64_t)(v.pitch() * v.mid) * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)o.chunk, (cuuint32_t)(o.mn_major ? kGemmBK : rows), (cuuint32_t)o.box};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        o.chunk == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : o.chunk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                        : CU_TENSOR_MAP_SWIZZLE_32B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MQV_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+  return MQV_OK;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <int BN>
+cudaError_t launch_gemm_bn(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
+  static bool done[kMaxDevices] = {};
+  const cudaError_t e = allow_smem(gemm_tc_kernel<BN>, gemm_smem<BN>, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)pl.args.tiles_m * pl.args.tiles_n * pl.args.splits;
+  gemm_tc_kernel<BN><<<(unsigned)std::min<int64_t>(tiles, kSms), kGemmThreads, gemm_smem<BN>, st>>>(ma, mb, pl.args);
+  return cudaGetLastError();
+}
+
+// Copies an operand whose rows are unaligned; *p then points at the copy.
+void repitch(const GemmView& v, const void** p, char** ws, cudaStream_t st) {
+  if (!v.copied()) return;
+  const int64_t rows = v.pos * v.mid, units = rows * (v.pitch() / 8);
+  repitch_kernel<<<(unsigned)std::min<int64_t>(ceil_div(units, 256), kSms * 16), 256, 0, st>>>(
+      static_cast<const uint16_t*>(*p), reinterpret_cast<uint16_t*>(*ws), rows, (int)v.inner, (int)v.pitch());
+  *p = *ws;
+  *ws += v.copy_bytes();
+}
+
+// The pass `op` with A and B at a and b, and epilogue e (its d, z, residual,
+// bias and act).
+mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b, const Epilogue& e, void* ws,
+                    cudaStream_t st) {
+  GemmPlan pl;
+  plan_gemm(d, op, &pl);
+  GemmTcArgs& g = pl.args;
+  if (pl.out_elems == 0) return ok();
+  if (g.kblocks == 0) {          // a weight gradient over no columns
+    const cudaError_t ce = cudaMemsetAsync(e.d.p, 0, (size_t)pl.out_elems * 4, st);
+    return ce == cudaSuccess ? ok() : cuda_fail(ce, "linear layer gradient");
+  }
+  const Epilogue plan_e = g.e;
+  g.e = e;
+  g.e.vec4 = plan_e.vec4;
+  g.e.bias_on_row = plan_e.bias_on_row;
+  char* w = static_cast<char*>(ws);
+  if (g.splits > 1) g.part = reinterpret_cast<float*>(w);
+  w += pl.part_bytes;
+  mqv_status s = device_error_word(&g.err);
+  if (s) return s;
+  CUtensorMap ma, mb;
+  repitch(pl.a, &a, &w, st);
+  repitch(pl.b, &b, &w, st);
+  if ((s = encode(&ma, a, pl.a, pl.oa, kGemmBM)) || (s = encode(&mb, b, pl.b, pl.ob, pl.bn))) return s;
+  cudaError_t ce = pl.bn == 256   ? launch_gemm_bn<256>(pl, ma, mb, st)
+                   : pl.bn == 128 ? launch_gemm_bn<128>(pl, ma, mb, st)
+                                  : launch_gemm_bn<64>(pl, ma, mb, st);
+  if (ce != cudaSuccess) return cuda_fail(ce, "linear layer launch");
+  if (g.splits > 1) {
+    const int64_t inner = g.e.bias_on_row ? g.col_inner : 1, channels = g.e.bias_on_row ? pl.M : g.col_inner;
+    const int v = g.e.vec4 ? 4 : 1;
+    const unsigned blocks = (unsigned)ceil_div(pl.out_elems, 256 * v);
+    if (v == 4)
+      split_sum_kernel<4><<<blocks, 256, 0, st>>>(g.e, g.part, g.splits, g.part_stride, pl.out_elems, inner, channels);
+    else
+      split_sum_kernel<1><<<blocks, 256, 0, st>>>(g.e, g.part, g.splits, g.part_stride, pl.out_elems, inner, channels);
+  }
   return launched("linear layer launch");
 }
 
-// D[channel][column] of a product over channels: rows are columns of the
-// tensor for token rows, channels otherwise, so that D's columns are
-// contiguous either way.
-void orient(GemmArgs* g, bool tokens, const void* w, Dim w_out, Dim w_k, int64_t out, const void* x, Dim x_col, Dim x_k,
-            int64_t cols, Dim d_ch, Dim d_col) {
-  const uint16_t *wp = static_cast<const uint16_t*>(w), *xp = static_cast<const uint16_t*>(x);
-  if (tokens) {
-    g->a = xp, g->a_row = x_col, g->a_k = x_k, g->b = wp, g->b_col = w_out, g->b_k = w_k;
-    g->M = cols, g->N = out, g->d_row = d_col, g->d_col = d_ch, g->bias_on_row = 0;
-  } else {
-    g->a = wp, g->a_row = w_out, g->a_k = w_k, g->b = xp, g->b_col = x_col, g->b_k = x_k;
-    g->M = out, g->N = cols, g->d_row = d_ch, g->d_col = d_col, g->bias_on_row = 1;
-  }
+int64_t lin_ws(const mqv_lin_desc* d, int op) {
+  if (op == MQV_OP_ACT_GRAD) return align256((int64_t)plan_act_grad(d).gy * d->Cout * 4);
+  GemmPlan pl;
+  plan_gemm(d, op, &pl);
+  return pl.out_elems && pl.args.kblocks ? pl.ws_bytes : 0;
 }
 
 }  // namespace
@@ -357,16 +548,13 @@ mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, cons
                            {"ws", ws, need, true, false}},
                           "y", "residual")))
     return st;
-  GemmArgs g = {};
-  orient(&g, d->N == 1, w, channel_dim(d->Cin), channel_dim(1), d->Cout, x, column_dim(d->Cin, d->N), channel_dim(d->N),
-         cols, channel_dim(d->N), column_dim(d->Cout, d->N));
-  g.K = d->Cin;
-  g.bias = bias;
-  g.residual = residual;
-  g.z = {z, 1};
-  g.d = {y, y_type == MQV_BF16};
-  g.act = d->act;
-  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+  Epilogue e = {};
+  e.d = {y, y_type == MQV_BF16};
+  e.z = {z, 1};
+  e.residual = residual;
+  e.bias = bias;
+  e.act = d->act;
+  return run_gemm(d, MQV_OP_FWD, d->N == 1 ? x : w, d->N == 1 ? w : x, e, ws, static_cast<cudaStream_t>(stream));
 }
 
 mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_type, const void* z, void* gz,
@@ -430,12 +618,9 @@ mqv_status mqv_lin_dgrad(const mqv_lin_desc* d, const void* w, const void* gz, v
                            {"gx", gx, cols * d->Cin * type_size(gx_type), true, true},
                            {"ws", ws, need, true, false}})))
     return st;
-  GemmArgs g = {};
-  orient(&g, d->N == 1, w, channel_dim(1), channel_dim(d->Cin), d->Cin, gz, column_dim(d->Cout, d->N),
-         channel_dim(d->N), cols, channel_dim(d->N), column_dim(d->Cin, d->N));
-  g.K = d->Cout;
-  g.d = {gx, gx_type == MQV_BF16};
-  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+  Epilogue e = {};
+  e.d = {gx, gx_type == MQV_BF16};
+  return run_gemm(d, MQV_OP_DGRAD, d->N == 1 ? gz : w, d->N == 1 ? w : gz, e, ws, static_cast<cudaStream_t>(stream));
 }
 
 mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, float* gw, void* ws, size_t ws_bytes,
@@ -449,20 +634,9 @@ mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, f
                            {"gw", gw, d->Cout * d->Cin * 4, true, true},
                            {"ws", ws, need, true, false}})))
     return st;
-  GemmArgs g = {};
-  g.a = static_cast<const uint16_t*>(gz);
-  g.a_row = channel_dim(d->N);
-  g.a_k = column_dim(d->Cout, d->N);
-  g.b = static_cast<const uint16_t*>(x);
-  g.b_col = channel_dim(d->N);
-  g.b_k = column_dim(d->Cin, d->N);
-  g.M = d->Cout;
-  g.N = d->Cin;
-  g.K = cols;
-  g.d = {gw, 0};
-  g.d_row = channel_dim(d->Cin);
-  g.d_col = channel_dim(1);
-  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+  Epilogue e = {};
+  e.d = {gw, 0};
+  return run_gemm(d, MQV_OP_WGRAD, gz, x, e, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -7,96 +7,71 @@
 // bfloat16, sums fp32.
 #pragma once
 
-#include "mqv_layer_common.cuh"
+#include "mqv_linear_act.cuh"
 
 namespace mqv {
 
-enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
+// ----------------------------------------------------- around the product
 
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;       // a NaN stays one
-    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case kActSilu: return z / (1.f + expf(-z));
-    default: return z;
-  }
-}
-
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * (0.3989422804014327f * expf(-0.5f * z * z));
-    case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
-    }
-    default: return 1.f;
-  }
-}
-
-// ------------------------------------------------ matrix product, one tile
-
-// Element offset of index i of one dimension: whole groups of `div` apart by
-// `outer`, items of a group apart by `inner`.
-struct Dim {
-  int64_t div, outer, inner;
-  __host__ __device__ int64_t at(int64_t i) const { return (i / div) * outer + (i % div) * inner; }
-};
-
-struct GemmArgs {
-  const uint16_t *a, *b;       // bf16
-  Dim a_row, a_k, b_col, b_k;
-  int64_t M, N, K;
-  TensorOut d, z;              // z.p null: not kept
-  const void* residual;        // of d's type; null: none
-  Dim d_row, d_col;
-  const float* bias;           // null: none
-  int bias_on_row, act;
-};
-
-// D[m][n] = epilogue(sum_k A[m][k]·B[k][n]), 64 x 64 outputs a block, 4 x 4 a
-// thread, K in steps of 16 through shared memory.
-__global__ void __launch_bounds__(256) gemm_simple_kernel(const GemmArgs g) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t tiles_n = (g.N + 63) / 64;
-  const int64_t m0 = (blockIdx.x / tiles_n) * 64, n0 = (blockIdx.x % tiles_n) * 64;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < g.K; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int r = i & 63, k = i >> 6;
-      const bool kin = k0 + k < g.K;
-      sa[k][r] = kin && m0 + r < g.M
-                     ? __uint_as_float(static_cast<uint32_t>(g.a[g.a_row.at(m0 + r) + g.a_k.at(k0 + k)]) << 16) : 0.f;
-      sb[k][r] = kin && n0 + r < g.N
-                     ? __uint_as_float(static_cast<uint32_t>(g.b[g.b_col.at(n0 + r) + g.b_k.at(k0 + k)]) << 16) : 0.f;
-    }
-    __syncthreads();
+// Rows of `len` elements copied to rows `pitch` apart (a multiple of 8), for
+// operands whose own rows do not start on the 16-byte boundaries that a TMA
+// load needs.  What lies between len and pitch is never read.  A thread
+// writes one 16-byte vector, from the two aligned source vectors around it.
+__global__ void __launch_bounds__(256)
+repitch_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst, int64_t rows, int len, int pitch) {
+  const int per = pitch / 8;
+  const int64_t total = rows * len, units = rows * per;
+  for (int64_t u = blockIdx.x * int64_t{256} + threadIdx.x; u < units; u += gridDim.x * int64_t{256}) {
+    const int64_t r = u / per;
+    const int c = static_cast<int>(u - r * per) * 8;
+    const int64_t i = r * len + c, i0 = i & ~int64_t{7};
+    const int sh = static_cast<int>(i - i0);
+    uint4 out;
+    if (i0 + 16 <= total) {
+      const uint4 lo = __ldg(reinterpret_cast<const uint4*>(src + i0));
+      const uint4 hi = sh ? __ldg(reinterpret_cast<const uint4*>(src + i0 + 8)) : lo;
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      uint32_t v[4];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a = 0, b = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= g.M || n >= g.N) continue;
-      const int64_t o = g.d_row.at(m) + g.d_col.at(n);
-      float v = acc[i][j];
-      if (g.bias) v += g.bias[g.bias_on_row ? m : n];
-      if (g.z.p) store_vec<1>(g.z, o, {v});
-      v = act_value(v, g.act);
-      if (g.residual) {
-        float r[1];
-        g.d.bf16 ? load_bf16<1>(g.residual, o, r) : load_f32<1>(g.residual, o, r);
-        v += r[0];
+        for (int j = 0; j < 8; ++j) {      // words of the 8 elements from sh on
+          if (j == (sh >> 1) + k) a = w[j];
+          if (j == (sh >> 1) + k + 1) b = w[j];
+        }
+        v[k] = (sh & 1) ? __funnelshift_r(a, b, 16) : a;
       }
-      store_vec<1>(g.d, o, {v});
+      out = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint16_t h[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = i + k < total ? __ldg(src + i + k) : uint16_t{0};
+      out = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     }
+    *reinterpret_cast<uint4*>(dst + r * pitch + c) = out;
+  }
+}
+
+// The sums of a product split along K, part[s][i], added in the order of s,
+// with the epilogue.  Element i's channel is (i / inner) % channels, as row
+// of the tile when the batch is `inner`, as column when inner = 1.
+template <int V>
+__global__ void __launch_bounds__(256)
+split_sum_kernel(const Epilogue e, const float* __restrict__ part, int splits, int64_t stride, int64_t n,
+                 int64_t inner, int64_t channels) {
+  const int64_t i = (blockIdx.x * int64_t{256} + threadIdx.x) * V;
+  if (i >= n) return;
+  float v[V] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    float t[V];
+    load_f32<V>(part, s * stride + i, t);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += t[j];
+  }
+  const int64_t ch = e.bias ? (i / inner) % channels : 0;
+  epilogue_store<V>(e, i, ch, ch, v);
 }
 
 // --------------------------------------- gradient of activation and bias
