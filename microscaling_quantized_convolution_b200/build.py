@@ -33,7 +33,7 @@ def _object_deps(src):
     them down beside it; every header where it has not."""
     try:
         with open(_object(src)[:-2] + ".d") as f:
-            words = f.read().replace("\\\n", " ").split()[1:]
+            words = f.read().split(":", 1)[1].replace("\\\n", " ").split()
     except OSError:
         return [os.path.join(CSRC, src)] + _headers()
     return [w for w in map(os.path.realpath, words) if w.startswith(os.path.realpath(ROOT) + os.sep)]

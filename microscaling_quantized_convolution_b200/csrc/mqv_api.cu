@@ -99,16 +99,6 @@ int64_t quant_ctas(int64_t rows, int64_t cols, int32_t blocks = MQV_BLOCKS_4X4) 
   return g < kMaxQuantCtas ? g : kMaxQuantCtas;
 }
 
-FastDiv make_fastdiv(int64_t d) {
-  FastDiv f;
-  uint32_t s = 0;
-  while ((int64_t(1) << s) < d) ++s;
-  const unsigned __int128 num = (static_cast<unsigned __int128>(1) << (32 + s)) + (d - 1);
-  f.m = static_cast<uint32_t>(static_cast<uint64_t>(num / static_cast<unsigned __int128>(d)) - (uint64_t(1) << 32));
-  f.s = s;
-  return f;
-}
-
 mqv_status check_view(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0 || rows % 4 || cols % 4)
     return fail(MQV_ERR_INVALID_ARG, "view %lld x %lld: rows and cols must be positive multiples of 4",

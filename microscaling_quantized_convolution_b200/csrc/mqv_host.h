@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "mqv.h"
+#include "mqv_ptx.cuh"
 
 namespace mqv {
 
@@ -21,5 +22,16 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // The current device's error word, which bounded waits set on timeout.
 mqv_status device_error_word(uint32_t** out);
+
+// The constants of a division by d (see FastDiv).
+inline FastDiv make_fastdiv(int64_t d) {
+  FastDiv f;
+  uint32_t s = 0;
+  while ((int64_t(1) << s) < d) ++s;
+  const unsigned __int128 num = (static_cast<unsigned __int128>(1) << (32 + s)) + (d - 1);
+  f.m = static_cast<uint32_t>(static_cast<uint64_t>(num / static_cast<unsigned __int128>(d)) - (uint64_t(1) << 32));
+  f.s = s;
+  return f;
+}
 
 }  // namespace mqv

@@ -47,6 +47,19 @@ __device__ __forceinline__ void load_f32(const void* p, int64_t i, float (&v)[V]
   }
 }
 
+// The same from memory that a kernel still running at this one's start wrote:
+// not through the read-only path.
+template <int V>
+__device__ __forceinline__ void load_cg(const float* f, float (&v)[V]) {
+  if constexpr (V == 4) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(f));
+    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = __ldcg(f + q);
+  }
+}
+
 template <int V>
 __device__ __forceinline__ void load_bf16(const void* p, int64_t i, float (&v)[V]) {
   const uint16_t* h = static_cast<const uint16_t*>(p) + i;

@@ -21,7 +21,7 @@ using namespace mqv;
 constexpr int kSms = 148;
 constexpr int64_t kMaxChannels = 16384;             // layer norm: a position's channels in one block's registers
 constexpr int64_t kMaxElements = int64_t{1} << 38;
-constexpr int64_t kMaxColumns = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxColumns = (int64_t{1} << 31) - (1 << 16);   // with a tile's overhang still an int
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t b) { return ceil_div(b, 256) * 256; }
@@ -197,9 +197,10 @@ mqv_status check_lin(const mqv_lin_desc* d) {
                 "linear layer [%lld][%lld -> %lld][%lld]: P >= 0, Cin, Cout and N > 0, reserved 0 required",
                 (long long)d->P, (long long)d->Cin, (long long)d->Cout, (long long)d->N);
   if (d->act < MQV_ACT_NONE || d->act > MQV_ACT_SILU) return fail(MQV_ERR_INVALID_ARG, "unknown activation %d", d->act);
-  const int64_t c = std::max(d->Cin, d->Cout);
-  if (c > (1 << 24) || d->N > kMaxColumns || d->P > kMaxColumns / d->N ||
-      (d->P > 0 && c > kMaxElements / (d->P * d->N)))
+  // a position's columns are padded to whole chunks in the tiles
+  const int64_t c = std::max(d->Cin, d->Cout), padded = d->N == 1 ? 1 : ceil_div(d->N, 64) * 64;
+  if (c > (1 << 24) || d->N > kMaxColumns - 64 || d->P > kMaxColumns / padded ||
+      (d->P > 0 && c > kMaxElements / (d->P * padded)))
     return fail(MQV_ERR_UNSUPPORTED, "linear layer [%lld][%lld -> %lld][%lld] too large", (long long)d->P,
                 (long long)d->Cin, (long long)d->Cout, (long long)d->N);
   return MQV_OK;
@@ -241,6 +242,9 @@ struct GemmView {
   int64_t pitch() const { return ceil_div(inner, 8) * 8; }
   bool copied() const { return inner % 8 != 0; }
   int64_t copy_bytes() const { return copied() ? align256(pos * mid * pitch() * 2) : 0; }
+  // a plain MN-major matrix of whole 64-element chunks: the chunks are taken
+  // as positions, so that one box brings a stage's share
+  bool chunked() const { return pos == 1 && mn_major && inner % 64 == 0; }
 };
 
 // One pass as D = A·B^T over the views; D's columns are contiguous.
@@ -249,6 +253,7 @@ struct GemmPlan {
   GemmOperand oa, ob;
   int64_t M;
   int bn;
+  bool pair;
   GemmTcArgs args;
   int64_t out_elems, part_bytes, ws_bytes;
 };
@@ -267,10 +272,45 @@ int chunk_of(int64_t inner) {
 GemmOperand operand_of(const GemmView& v, int rows, bool batch) {
   GemmOperand o;
   o.chunk = batch ? chunk_of(v.inner) : 64;
-  o.per_pos = (int)ceil_div(v.inner, o.chunk);
+  o.per_pos = v.chunked() ? 1 : (int)ceil_div(v.inner, o.chunk);
   o.mn_major = v.mn_major;
-  o.box = batch && o.per_pos == 1 ? (v.mn_major ? rows : kGemmBK) / o.chunk : 1;
+  o.box = (batch || v.chunked()) && o.per_pos == 1 ? (v.mn_major ? rows : kGemmBK) / o.chunk : 1;
   return o;
+}
+
+// The tile and the split of K with the least time by a model of the measured
+// times (us): a launch of one wave of tiles takes `base` (launch, first loads,
+// last epilogue) and `block` a K block; a wave is no shorter than the epilogue
+// that it overlaps with.  Measured at 8192 tokens 4096 -> 4096: 166 us in
+// 256 x 256 tiles of two CTAs, 279 in 128 x 128, 527 in 128 x 64; at 128
+// tokens 1024 -> 1024: 14.3, 10.8 and 8.8; 256 x 128 tiles of two CTAs were
+// never faster than 128 x 128.  A split writes and reads fp32 partial sums
+// and takes a second kernel.
+void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
+  struct Tile {
+    int bn;
+    bool pair;
+    double base, block, epilogue;
+  };
+  static constexpr Tile kTiles[] = {{256, true, 9.2, .37, 4.6}, {128, false, 6.0, .31, 2.4}, {64, false, 4.5, .29, 1.2}};
+  double best = 0;
+  for (const Tile& t : kTiles) {
+    const int64_t units = t.pair ? kSms / 2 : kSms;
+    const int64_t tiles = std::max<int64_t>(1, ceil_div(pl->M, t.pair ? 2 * kGemmBM : kGemmBM) * ceil_div(vcols, t.bn));
+    const int64_t fill = std::max<int64_t>(1, std::min(units / tiles, kblocks / 2));
+    for (int64_t s : {int64_t{1}, int64_t{2}, int64_t{4}, int64_t{8}, int64_t{16}, int64_t{32}, fill}) {
+      if (s > fill) continue;
+      const double wave = std::max(ceil_div(kblocks, s) * t.block, t.epilogue);
+      double us = t.base + ceil_div(tiles * s, units) * wave;
+      if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.5e6;
+      if (best == 0 || us < best) {
+        best = us;
+        pl->bn = t.bn;
+        pl->pair = t.pair;
+        pl->args.splits = (int)s;
+      }
+    }
+  }
 }
 
 void plan_gemm(const mqv_lin_desc* d, int op, GemmPlan* pl) {
@@ -310,6 +350,7 @@ void plan_gemm(const mqv_lin_desc* d, int op, GemmPlan* pl) {
   const bool col_batch = op != MQV_OP_WGRAD && !tokens;
   g.M = pl->M;
   g.col_chunk = col_batch ? chunk_of(d->N) : 64;
+  g.col_shift = g.col_chunk == 64 ? 6 : g.col_chunk == 32 ? 5 : 4;
   g.col_inner = col_batch ? d->N : cols;
   g.col_pos = col_batch ? d->P : 1;
   g.col_per_pos = (int)ceil_div(g.col_inner, g.col_chunk);
@@ -319,20 +360,22 @@ void plan_gemm(const mqv_lin_desc* d, int op, GemmPlan* pl) {
   g.e.bias_on_row = col_batch;
   pl->out_elems = pl->M * g.col_inner * g.col_pos;
   const int64_t vcols = g.col_pos * g.col_per_pos * g.col_chunk;
-  pl->bn = vcols <= 64 ? 64 : vcols <= 128 ? 128 : 256;
-  g.tiles_m = (int)ceil_div(pl->M, kGemmBM);
-  // narrower tiles while the wide ones leave half of the SMs without work
-  while (pl->bn > 64 && g.tiles_m * ceil_div(vcols, pl->bn) * 2 <= kSms) pl->bn /= 2;
+  const int64_t kblocks = kdim ? ceil_div(kdim, kGemmBK)
+                          : batch_a ? ceil_div(d->P * ceil_div(d->N, chunk_of(d->N)), kGemmBK / chunk_of(d->N))
+                                    : ceil_div(d->P, kGemmBK);
+  choose_tile(pl, kblocks, vcols);
+  g.tiles_m = (int)ceil_div(pl->M, pl->pair ? 2 * kGemmBM : kGemmBM);
   g.tiles_n = (int)ceil_div(vcols, pl->bn);
+  g.tail_width = g.tiles_n % 8 ? g.tiles_n % 8 : 8;
+  g.by_split = make_fastdiv(std::max<int64_t>(1, (int64_t)g.tiles_m * g.tiles_n));
+  g.by_band = make_fastdiv(std::max<int64_t>(1, (int64_t)g.tiles_m * 8));
+  g.by_tail = make_fastdiv(g.tail_width);
+  g.by_pos = make_fastdiv(std::max(1, g.col_per_pos));
   pl->oa = operand_of(pl->a, kGemmBM, batch_a);
-  pl->ob = operand_of(pl->b, pl->bn, batch_b);
+  pl->ob = operand_of(pl->b, pl->pair ? pl->bn / 2 : pl->bn, batch_b);
   g.a = pl->oa;
   g.b = pl->ob;
-  g.kblocks = (int)(kdim ? ceil_div(kdim, kGemmBK)
-                         : batch_a ? ceil_div(d->P * pl->oa.per_pos, kGemmBK / pl->oa.chunk) : ceil_div(d->P, kGemmBK));
-  // split K while tiles leave SMs idle and a split keeps four K blocks
-  const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-  g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(tiles, 1), g.kblocks / 4));
+  g.kblocks = (int)kblocks;
   g.part_stride = ceil_div(pl->out_elems, 4) * 4;
   pl->part_bytes = g.splits > 1 ? align256(g.splits * g.part_stride * 4) : 0;
   pl->ws_bytes = pl->part_bytes + pl->a.copy_bytes() + pl->b.copy_bytes();
@@ -354,21 +397,39 @@ EncodeFn tensor_map_encoder() {
   return fn;
 }
 
-mqv_status encode(CUtensorMap* map, const void* p, const GemmView& v, const GemmOperand& o, int rows) {
+mqv_status encode(CUtensorMap* map, bool f32, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
   const EncodeFn fn = tensor_map_encoder();
   if (!fn) return fail(MQV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from this driver");
-  const cuuint64_t dims[3] = {(cuuint64_t)v.inner, (cuuint64_t)v.mid, (cuuint64_t)v.pos};
-  const cuuint64_t strides[2] = {(cuuint64_t)v.pitch() * 2, (cuuint64_t)(v.pitch() * v.mid) * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)o.chunk, (cuuint32_t)(o.mn_major ? kGemmBK : rows), (cuuint32_t)o.box};
-  const cuuint32_t ones[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, ones,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        o.chunk == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                        : o.chunk == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                        : CU_TENSOR_MAP_SWIZZLE_32B,
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const unsigned span = box[0] * (f32 ? 4 : 2);
+  const CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                        const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MQV_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
   return MQV_OK;
+}
+
+mqv_status encode_operand(CUtensorMap* map, const void* p, const GemmView& v, const GemmOperand& o, int rows) {
+  const bool ch = v.chunked();
+  const cuuint64_t dims[3] = {(cuuint64_t)(ch ? 64 : v.inner), (cuuint64_t)v.mid, (cuuint64_t)(ch ? v.inner / 64 : v.pos)};
+  const cuuint64_t strides[2] = {(cuuint64_t)v.pitch() * 2, (cuuint64_t)(ch ? 64 : v.pitch() * v.mid) * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)o.chunk, (cuuint32_t)(o.mn_major ? kGemmBK : rows), (cuuint32_t)o.box};
+  return encode(map, false, 3, p, dims, strides, box);
+}
+
+// An output (or the residual) in staged tiles of 32 rows x 32 columns; the
+// fourth dimension is the split of the partial sums.
+mqv_status encode_output(CUtensorMap* map, const void* p, bool f32, const GemmTcArgs& g) {
+  const int64_t size = f32 ? 4 : 2, width = std::min(g.col_chunk, 32);
+  const int64_t row = g.row_stride * size, pos = g.M * row;
+  const cuuint64_t dims[4] = {(cuuint64_t)g.col_inner, (cuuint64_t)g.M, (cuuint64_t)g.col_pos, (cuuint64_t)g.splits};
+  const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)pos, (cuuint64_t)(g.splits > 1 ? g.part_stride * size : 16)};
+  const cuuint32_t box[4] = {(cuuint32_t)width, 32, (cuuint32_t)(g.col_per_pos == 1 ? 32 / width : 1), 1};
+  return encode(map, f32, 4, p, dims, strides, box);
 }
 
 template <typename K>
@@ -383,14 +444,32 @@ cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
   return e;
 }
 
-template <int BN>
-cudaError_t launch_gemm_bn(const GemmPlan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
+template <int BN, bool PAIR, bool FAST>
+cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
-  const cudaError_t e = allow_smem(gemm_tc_kernel<BN>, gemm_smem<BN>, done);
+  auto kernel = gemm_tc_kernel<BN, PAIR, FAST>;
+  const cudaError_t e = allow_smem(kernel, gemm_smem<BN, PAIR, FAST>, done);
   if (e != cudaSuccess) return e;
+  constexpr int kCtas = PAIR ? 2 : 1;
   const int64_t tiles = (int64_t)pl.args.tiles_m * pl.args.tiles_n * pl.args.splits;
-  gemm_tc_kernel<BN><<<(unsigned)std::min<int64_t>(tiles, kSms), kGemmThreads, gemm_smem<BN>, st>>>(ma, mb, pl.args);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = (unsigned)(std::min<int64_t>(tiles, kSms / kCtas) * kCtas);
+  cfg.blockDim = kGemmThreads;
+  cfg.dynamicSmemBytes = gemm_smem<BN, PAIR, FAST>;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, pl.args);
+}
+
+template <bool FAST>
+cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
+  if (pl.pair) return launch_gemm_tile<256, true, FAST>(pl, maps, st);
+  return pl.bn == 128 ? launch_gemm_tile<128, false, FAST>(pl, maps, st) : launch_gemm_tile<64, false, FAST>(pl, maps, st);
 }
 
 // Copies an operand whose rows are unaligned; *p then points at the copy.
@@ -424,22 +503,39 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
   w += pl.part_bytes;
   mqv_status s = device_error_word(&g.err);
   if (s) return s;
-  CUtensorMap ma, mb;
+  GemmMaps maps;
   repitch(pl.a, &a, &w, st);
   repitch(pl.b, &b, &w, st);
-  if ((s = encode(&ma, a, pl.a, pl.oa, kGemmBM)) || (s = encode(&mb, b, pl.b, pl.ob, pl.bn))) return s;
-  cudaError_t ce = pl.bn == 256   ? launch_gemm_bn<256>(pl, ma, mb, st)
-                   : pl.bn == 128 ? launch_gemm_bn<128>(pl, ma, mb, st)
-                                  : launch_gemm_bn<64>(pl, ma, mb, st);
+  if ((s = encode_operand(&maps.a, a, pl.a, pl.oa, kGemmBM)) ||
+      (s = encode_operand(&maps.b, b, pl.b, pl.ob, pl.pair ? pl.bn / 2 : pl.bn)))
+    return s;
+  // rows of whole 16-byte vectors, in bfloat16 too: outputs go by TMA
+  const bool fast = g.col_inner % 8 == 0;
+  if (fast) {
+    if ((s = encode_output(&maps.d, g.part ? g.part : g.e.d.p, g.part || !g.e.d.bf16, g))) return s;
+    if (!g.part && g.e.z.p && (s = encode_output(&maps.z, g.e.z.p, false, g))) return s;
+    if (!g.part && g.e.residual && (s = encode_output(&maps.residual, g.e.residual, !g.e.d.bf16, g))) return s;
+  }
+  const cudaError_t ce = fast ? launch_gemm<true>(pl, maps, st) : launch_gemm<false>(pl, maps, st);
   if (ce != cudaSuccess) return cuda_fail(ce, "linear layer launch");
   if (g.splits > 1) {
     const int64_t inner = g.e.bias_on_row ? g.col_inner : 1, channels = g.e.bias_on_row ? pl.M : g.col_inner;
     const int v = g.e.vec4 ? 4 : 1;
-    const unsigned blocks = (unsigned)ceil_div(pl.out_elems, 256 * v);
-    if (v == 4)
-      split_sum_kernel<4><<<blocks, 256, 0, st>>>(g.e, g.part, g.splits, g.part_stride, pl.out_elems, inner, channels);
-    else
-      split_sum_kernel<1><<<blocks, 256, 0, st>>>(g.e, g.part, g.splits, g.part_stride, pl.out_elems, inner, channels);
+    const unsigned blocks = (unsigned)ceil_div(pl.out_elems, 32 * v);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = blocks;
+    cfg.blockDim = 256;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const float* part = g.part;
+    const cudaError_t se =
+        v == 4 ? cudaLaunchKernelEx(&cfg, split_sum_kernel<4>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels)
+               : cudaLaunchKernelEx(&cfg, split_sum_kernel<1>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels);
+    if (se != cudaSuccess) return cuda_fail(se, "linear layer launch");
   }
   return launched("linear layer launch");
 }

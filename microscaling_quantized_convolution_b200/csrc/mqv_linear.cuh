@@ -8,6 +8,7 @@
 #pragma once
 
 #include "mqv_linear_act.cuh"
+#include "mqv_ptx.cuh"
 
 namespace mqv {
 
@@ -53,23 +54,36 @@ repitch_kernel(const uint16_t* __restrict__ src, uint16_t* __restrict__ dst, int
   }
 }
 
-// The sums of a product split along K, part[s][i], added in the order of s,
-// with the epilogue.  Element i's channel is (i / inner) % channels, as row
-// of the tile when the batch is `inner`, as column when inner = 1.
+// The sums of a product split along K, part[s][i], with the epilogue: a block
+// takes 32·V elements, warp q the splits q, q + 8, ...; the eight parts are
+// added in order.  Element i's channel is (i / inner) % channels, as row of
+// the tile when the batch is `inner`, as column when inner = 1.  Launched as a
+// programmatic dependent of the product.
 template <int V>
 __global__ void __launch_bounds__(256)
 split_sum_kernel(const Epilogue e, const float* __restrict__ part, int splits, int64_t stride, int64_t n,
                  int64_t inner, int64_t channels) {
-  const int64_t i = (blockIdx.x * int64_t{256} + threadIdx.x) * V;
-  if (i >= n) return;
+  __shared__ float s[8][32 * V];
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int64_t i = (blockIdx.x * int64_t{32} + lane) * V;
+  pdl_wait_prerequisite();
   float v[V] = {};
+  if (i < n)
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    float t[V];
-    load_f32<V>(part, s * stride + i, t);
+    for (int k = q; k < splits; k += 8) {
+      float t[V];
+      load_cg<V>(part + k * stride + i, t);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] += t[j];
-  }
+      for (int j = 0; j < V; ++j) v[j] += t[j];
+    }
+#pragma unroll
+  for (int j = 0; j < V; ++j) s[q][lane * V + j] = v[j];
+  __syncthreads();
+  if (q > 0 || i >= n) return;
+  const int parts = splits < 8 ? splits : 8;
+  for (int r = 1; r < parts; ++r)
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += s[r][lane * V + j];
   const int64_t ch = e.bias ? (i / inner) % channels : 0;
   epilogue_store<V>(e, i, ch, ch, v);
 }

@@ -8,11 +8,42 @@ namespace mqv {
 
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Phi(z), the normal distribution function, and phi = exp(-z^2 / 2).
+// erf by Hastings' approximation (Abramowitz and Stegun 7.1.26): with t =
+// 1 / (1 + 0.3275911·x), x = |z| / sqrt 2, 1 - erf(x) = t·poly4(t)·exp(-x^2)
+// within 1.5e-7, 0.75e-7 of Phi: less than two roundings of 1 + erf.  Two
+// special-function operations and about a dozen multiply-adds a value; the
+// library's erff costs three times that, more than the products of a tile
+// with 1024 channels.
+__device__ __forceinline__ float normal_cdf(float z, float* phi) {
+  const float t = __fdividef(1.f, fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  const float e = exp2_approx(z * z * -0.72134752f);       // -log2(e) / 2
+  *phi = e;
+  const float tail = 0.5f * t * q * e;
+  return z < 0.f ? tail : 1.f - tail;
+}
+
+// 1 / (1 + exp(-z)); exp overflows to infinity for z < -88, where the result is 0.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __fdividef(1.f, 1.f + exp2_approx(z * -1.44269504f));
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
+  float phi;
   switch (act) {
     case kActRelu: return z < 0.f ? 0.f : z;       // a NaN stays one
-    case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case kActSilu: return z / (1.f + expf(-z));
+    case kActGelu: return z * normal_cdf(z, &phi);
+    case kActSilu: return z * sigmoid(z);
     default: return z;
   }
 }
@@ -20,13 +51,31 @@ __device__ __forceinline__ float act_value(float z, int act) {
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * (0.3989422804014327f * expf(-0.5f * z * z));
+    case kActGelu: {
+      float phi;
+      const float c = normal_cdf(z, &phi);
+      return fmaf(z * 0.39894228f, phi, c);
+    }
     case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
+      const float s = sigmoid(z);
+      return s * fmaf(z, 1.f - s, 1.f);
     }
     default: return 1.f;
+  }
+}
+
+// The activation of K values, its kind tested once.
+template <int K>
+__device__ __forceinline__ void act_values(float (&v)[K], int act) {
+  if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActGelu);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActSilu);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActRelu);
   }
 }
 

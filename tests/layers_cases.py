@@ -18,6 +18,9 @@ LIN_TOKENS = [(1, 1, 1, 1), (1, 64, 64, 1), (1, 1000, 1003, 1), (2, 2048, 96, 1)
 LIN_PIXELS = [(1, 3, 5, 2), (7, 16, 8, 4), (49, 64, 64, 16), (5, 33, 40, 12), (4, 128, 256, 64), (3, 64, 100, 84),
               (10, 24, 24, 8), (3, 40, 48, 32), (2, 16, 16, 200), (6, 65, 63, 16), (1, 128, 128, 96), (30, 64, 128, 24),
               (1, 200, 72, 7), (100, 16, 24, 16), (2, 136, 320, 128)]
+# enough tiles for two-CTA tiles of 256 x 256 or 256 x 128 in one pass or another
+LIN_WIDE = [(2500, 40, 1992, 1), (2300, 72, 2047, 1), (1300, 64, 1608, 1), (65, 1992, 2500, 1), (600, 264, 280, 16),
+            (300, 264, 520, 32), (150, 260, 264, 64), (150, 264, 296, 80)]
 
 
 def shape_id(s):

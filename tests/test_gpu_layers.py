@@ -7,7 +7,7 @@ import torch
 
 import microscaling_quantized_convolution_b200 as mqv
 from oracle import layers_oracle as L
-from tests.layers_cases import LIN_PIXELS, LIN_TOKENS, LN_ROWS, LN_TILES, activations, shape_id, stored
+from tests.layers_cases import LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES, activations, shape_id, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -148,7 +148,7 @@ def lin_inputs(shape, seed=0):
             rng.standard_normal((P, Cout, N)), rng.standard_normal((P, Cout, N)) * 1e-2)
 
 
-@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS, ids=shape_id)
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE, ids=shape_id)
 def test_linear_layer(shape):
     P, Cin, Cout, N = shape
     w, x, bias, res, gy = lin_inputs(shape)
@@ -210,7 +210,11 @@ def test_activation_extremes():
         y, _ = mqv.lin_fwd(d, one, z, y_dtype=F32)
         s, _ = mqv.lin_act_grad(d, gy, z)
         zf = z.double().cpu().numpy()[:6]
-        check(y[:6], (L.act_value(zf, act), 24 * L.U * np.abs(zf) * (zf > -60)), act)
+        # below -60 only exp(z) is left of the value: its argument z·log2(e), rounded
+        # by U relative, is off by U·|z|·log2(e) absolute, so exp2 of it by U·|z|
+        # relative (ln 2·log2 e = 1), plus at most 8 U for exp2, sum and division
+        v = L.act_value(zf, act)
+        check(y[:6], (v, 24 * L.U * np.abs(zf) * (zf > -60) + (np.abs(zf) + 8) * L.U * np.abs(v) * (zf > -1e9)), act)
         check(s[:6], (L.act_slope(zf, act), np.full_like(zf, 16 * L.U)), act)
         assert torch.isnan(y[6, 0, 0]) and (act == "relu" or torch.isnan(s[6, 0, 0]))
 
