@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "mqv_ptx.cuh"
+
 namespace mqv {
 
 // A [P][C][N] tensor of either type.
@@ -108,25 +110,26 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sums of a parameter gradient's partial rows, part[b][i] for b < rows, in
-// the order of b within each of 8 fixed parts: out0 takes i < n, out1 (which
-// may be null) the n after them.  A block of 256 sums 32 columns.
-__global__ void __launch_bounds__(256)
+// the order of b within each of 32 fixed parts: out0 takes i < n, out1 (which
+// may be null) the n after them.  A block of 1024 sums 32 columns.  Launched
+// as a programmatic dependent of the kernel that writes the rows.
+__global__ void __launch_bounds__(1024)
 column_sum_kernel(const float* __restrict__ part, int rows, int64_t n, int pairs, float* __restrict__ out0,
                   float* __restrict__ out1) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane, width = n * pairs;
+  pdl_wait_prerequisite();
   float a = 0.f;
   if (i < width)
-    for (int b = q; b < rows; b += 8) a += __ldcg(part + b * width + i);
+#pragma unroll 4
+    for (int b = q; b < rows; b += 32) a += __ldcg(part + b * width + i);
   s[q][lane] = a;
   __syncthreads();
-  if (q == 0 && i < width) {
-    float t = 0.f;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) t += s[r][lane];
-    (i < n ? out0 + i : out1 + (i - n))[0] = t;
-  }
+  // warp q adds column q's 32 parts
+  const float t = warp_sum(s[lane][q]);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + q;
+  if (lane == 0 && c < width) (c < n ? out0 + c : out1 + (c - n))[0] = t;
 }
 
 }  // namespace mqv

@@ -71,23 +71,51 @@ mqv_status launched(const char* what) {
   return e == cudaSuccess ? ok() : cuda_fail(e, what);
 }
 
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+// Launch configuration with the attribute of a programmatic dependent.
+struct DependentLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  DependentLaunch(unsigned grid, unsigned block, cudaStream_t st) {
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
 void launch_column_sum(const float* part, int64_t rows, int64_t n, int pairs, float* out0, float* out1,
                        cudaStream_t st) {
-  column_sum_kernel<<<(unsigned)ceil_div(n * pairs, 32), 256, 0, st>>>(part, (int)rows, n, pairs, out0, out1);
+  DependentLaunch l((unsigned)ceil_div(n * pairs, 32), 1024, st);
+  cudaLaunchKernelEx(&l.cfg, column_sum_kernel, part, (int)rows, n, pairs, out0, out1);   // its error: launched()
 }
 
 // ------------------------------------------------------------- layer norm
 
-// Launch geometry of one direction: vector width, vectors per thread, threads
-// per block, and (N > 1) the tile.
+// Launch geometry of one direction: values and items per thread, threads of a
+// group, groups of a block and (N > 1) the tile.
 struct LnPlan {
-  int v, k, threads;
+  int v, k, group, groups;     // v: vector width; rows of scalars (v = 1) hold 2·k
   int tn, tiles, lanes, rows;
-  int64_t units;                 // rows or tiles
-  int64_t bwd_blocks;
+  int64_t units, blocks;
+  int threads() const { return group * groups; }
 };
 
-mqv_status plan_ln(const mqv_ln_desc* d, LnPlan* pl) {
+mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
   if (!d) return fail(MQV_ERR_INVALID_ARG, "null descriptor");
   if (d->P < 0 || d->C <= 0 || d->N <= 0 || d->reserved)
     return fail(MQV_ERR_INVALID_ARG, "layer norm of [%lld][%lld][%lld]: P >= 0, C and N > 0, reserved 0 required",
@@ -98,77 +126,133 @@ mqv_status plan_ln(const mqv_ln_desc* d, LnPlan* pl) {
   if (d->N > kMaxColumns || d->P > kMaxColumns / d->N || (d->P > 0 && d->C > kMaxElements / (d->P * d->N)))
     return fail(MQV_ERR_UNSUPPORTED, "tensor [%lld][%lld][%lld] too large", (long long)d->P, (long long)d->C,
                 (long long)d->N);
+  *pl = {};
   if (d->N == 1) {
-    // 8 values a thread up to 2048 channels, 16 above
-    const int e = d->C <= 2048 ? 8 : 16;
+    // 16 values per thread, which with their parameters (and backward the
+    // parameters' gradients) is what registers hold at 512 to 768 threads an
+    // SM; 8 for short rows
     pl->v = d->C % 8 == 0 ? 8 : 1;
-    pl->k = e / pl->v;
-    pl->threads = (int)(ceil_div(ceil_div(d->C, e), 32) * 32);
+    const int e = d->C <= 256 ? 8 : 16;
+    pl->k = pl->v == 8 ? e / 8 : e / 2;
+    pl->group = (int)(ceil_div(ceil_div(d->C, e), 32) * 32);
     pl->units = d->P;
-    pl->tn = pl->tiles = pl->lanes = pl->rows = 0;
   } else {
-    // 16 values a thread; the widest vectors and the widest tile (up to 64
-    // batch items) whose channels fit in one block
-    pl->threads = 0;
-    for (int v : {8, 4, 1}) {
-      if (d->N % v) continue;
-      const int k = 16 / v;
+    // K items of 4 (or 1) batch items a thread; the widest tile (up to 64
+    // batch items) whose channels fit in 512 threads, or in 1024 once its
+    // rows are down to 16 items
+    for (int v : {4, 1}) {
+      if (d->N % v || pl->group) continue;
+      const int k = v == 1 ? 16 : 8;
       for (int64_t tiles = ceil_div(d->N, 64);; tiles *= 2) {
         const int64_t tn = ceil_div(ceil_div(d->N, tiles), v) * v;
-        const int64_t lanes = tn / v, threads = ceil_div(lanes * ceil_div(d->C, k), 32) * 32;
-        if (threads <= kLnMaxThreads) {
+        const int64_t lanes = tn / v, group = ceil_div(lanes * ceil_div(d->C, k), 32) * 32;
+        if (group <= 512 || (group <= 1024 && tn <= 16)) {
           pl->v = v;
           pl->k = k;
-          pl->threads = (int)threads;
+          pl->group = (int)group;
           pl->tn = (int)tn;
           pl->tiles = (int)ceil_div(d->N, tn);
           pl->lanes = (int)lanes;
-          pl->rows = (int)(threads / lanes);
+          pl->rows = (int)std::min<int64_t>(group / lanes, d->C);
           break;
         }
         if (tn <= v) break;
       }
-      if (pl->threads) break;
     }
-    if (!pl->threads) return fail(MQV_ERR_UNSUPPORTED, "%lld channels", (long long)d->C);
+    if (!pl->group) return fail(MQV_ERR_UNSUPPORTED, "%lld channels", (long long)d->C);
     pl->units = d->P * pl->tiles;
   }
-  pl->bwd_blocks = std::min<int64_t>(pl->units, (int64_t)kSms * std::max(1, 1024 / pl->threads));
+  // Rows, and tiles backward, run as many blocks as fit (768 threads an SM
+  // forward, 512 backward, or one block), each over many units.  Backward,
+  // blocks of 256 threads hold several groups, since each block's partial row
+  // is to be added.
+  pl->groups = bwd ? std::max(1, 256 / pl->group) : pl->group == 32 ? 4 : 1;
+  pl->blocks = ceil_div(pl->units, pl->groups);
+  if (bwd || d->N == 1) {
+    const int64_t fit = pl->threads() > 256 ? 1 : (bwd ? 512 : 768) / pl->threads();
+    pl->blocks = std::min<int64_t>(pl->blocks, kSms * fit);
+  }
   return MQV_OK;
 }
 
-template <bool BWD, int V, int K, int T>
-void launch_ln_t(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
-  const unsigned grid = (unsigned)(BWD ? pl.bwd_blocks : pl.units);
-  if (rows) {
-    if (BWD)
-      ln_bwd_row_kernel<V, K, T><<<grid, pl.threads, 0, st>>>(a);
-    else
-      ln_fwd_row_kernel<V, K, T><<<grid, pl.threads, 0, st>>>(a);
-  } else {
-    const size_t smem = (size_t)pl.threads * std::max(V, 2) * sizeof(float);
-    if (BWD)
-      ln_bwd_tile_kernel<V, K, T><<<grid, pl.threads, smem, st>>>(a);
-    else
-      ln_fwd_tile_kernel<V, K, T><<<grid, pl.threads, smem, st>>>(a);
+template <typename K>
+cudaError_t launch_ln_kernel(K kernel, const LnArgs& a, const LnPlan& pl, int64_t smem, bool (&done)[kMaxDevices],
+                             cudaStream_t st) {
+  const cudaError_t e = allow_smem(kernel, 200 * 1024, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)pl.blocks, pl.threads(), (size_t)smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+int64_t slot_bytes(const TensorIn& t, const LnPlan& pl, int depth) {
+  return pl.v == 8 ? (int64_t)depth * pl.k * pl.threads() * (t.bf16 ? 16 : 32) : 0;
+}
+
+template <bool VEC, int K, int T, int B, bool KEEP>
+cudaError_t launch_ln_fwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+  static bool done[kMaxDevices] = {};
+  return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP>, a, pl, slot_bytes(a.x, pl, 3), done, st);
+}
+
+// The partial row is put together where the slots (or tiles' sums) were.
+template <bool VEC, int K, int T, int B, int D>
+cudaError_t launch_ln_bwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+  static bool done[kMaxDevices] = {};
+  return launch_ln_kernel(ln_bwd_row_kernel<VEC, K, T, B, D>, a, pl,
+                          std::max(slot_bytes(a.x, pl, D) + slot_bytes(a.gy, pl, D), 2 * (int64_t)a.C * 4), done, st);
+}
+
+template <int V, int K, int T>
+cudaError_t launch_ln_fwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+  static bool done[kMaxDevices] = {};
+  const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, V);
+  return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T>, a, pl, sums, done, st);
+}
+
+template <int V, int K, int T, int B>
+cudaError_t launch_ln_bwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+  static bool done[kMaxDevices] = {};
+  const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, 2 * V);
+  return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, st);
+}
+
+cudaError_t launch_ln_fwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+  const int t = pl.threads();
+  if (rows && pl.v == 8) {
+    if (pl.k == 1) return launch_ln_fwd_rows<true, 1, 128, 6, true>(a, pl, st);
+    return t <= 256   ? launch_ln_fwd_rows<true, 2, 256, 3, true>(a, pl, st)
+           : t <= 512 ? launch_ln_fwd_rows<true, 2, 512, 1, true>(a, pl, st)
+                      : launch_ln_fwd_rows<true, 2, 1024, 1, false>(a, pl, st);
   }
+  if (rows) {
+    if (pl.k == 4) return launch_ln_fwd_rows<false, 4, 128, 6, true>(a, pl, st);
+    return t <= 256   ? launch_ln_fwd_rows<false, 8, 256, 3, true>(a, pl, st)
+           : t <= 512 ? launch_ln_fwd_rows<false, 8, 512, 1, true>(a, pl, st)
+                      : launch_ln_fwd_rows<false, 8, 1024, 1, false>(a, pl, st);
+  }
+  if (pl.v == 4) return t <= 512 ? launch_ln_fwd_tiles<4, 8, 512>(a, pl, st) : launch_ln_fwd_tiles<4, 8, 1024>(a, pl, st);
+  return t <= 512 ? launch_ln_fwd_tiles<1, 16, 512>(a, pl, st) : launch_ln_fwd_tiles<1, 16, 1024>(a, pl, st);
 }
 
-template <bool BWD, int V, int K>
-void launch_ln_k(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
-  if (pl.threads <= kLnFewThreads)
-    launch_ln_t<BWD, V, K, kLnFewThreads>(a, pl, rows, st);
-  else
-    launch_ln_t<BWD, V, K, kLnMaxThreads>(a, pl, rows, st);
-}
-
-template <bool BWD>
-void launch_ln(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
-  if (pl.v == 8 && pl.k == 1) launch_ln_k<BWD, 8, 1>(a, pl, rows, st);
-  if (pl.v == 8 && pl.k == 2) launch_ln_k<BWD, 8, 2>(a, pl, rows, st);
-  if (pl.v == 4) launch_ln_k<BWD, 4, 4>(a, pl, rows, st);
-  if (pl.v == 1 && pl.k == 8) launch_ln_k<BWD, 1, 8>(a, pl, rows, st);
-  if (pl.v == 1 && pl.k == 16) launch_ln_k<BWD, 1, 16>(a, pl, rows, st);
+cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+  const int t = pl.threads();
+  if (rows && pl.v == 8) {
+    if (pl.k == 1) return launch_ln_bwd_rows<true, 1, 256, 2, 3>(a, pl, st);
+    return t <= 256   ? launch_ln_bwd_rows<true, 2, 256, 2, 3>(a, pl, st)
+           : t <= 512 ? launch_ln_bwd_rows<true, 2, 512, 1, 3>(a, pl, st)
+                      : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, st);
+  }
+  if (rows) {
+    if (pl.k == 4) return launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, st);
+    return t <= 256   ? launch_ln_bwd_rows<false, 8, 256, 2, 1>(a, pl, st)
+           : t <= 512 ? launch_ln_bwd_rows<false, 8, 512, 1, 1>(a, pl, st)
+                      : launch_ln_bwd_rows<false, 8, 1024, 1, 1>(a, pl, st);
+  }
+  if (pl.v == 4)
+    return t <= 256   ? launch_ln_bwd_tiles<4, 8, 256, 2>(a, pl, st)
+           : t <= 512 ? launch_ln_bwd_tiles<4, 8, 512, 1>(a, pl, st)
+                      : launch_ln_bwd_tiles<4, 8, 1024, 1>(a, pl, st);
+  return t <= 512 ? launch_ln_bwd_tiles<1, 16, 512, 1>(a, pl, st) : launch_ln_bwd_tiles<1, 16, 1024, 1>(a, pl, st);
 }
 
 LnArgs ln_args(const mqv_ln_desc* d, const LnPlan& pl, const void* x, int32_t x_type, const float* gamma) {
@@ -179,14 +263,17 @@ LnArgs ln_args(const mqv_ln_desc* d, const LnPlan& pl, const void* x, int32_t x_
   a.eps = d->eps;
   a.gamma = gamma;
   a.x = {x, x_type == MQV_BF16};
+  a.group = pl.group;
+  a.units = (int)pl.units;
   a.tn = pl.tn;
   a.tiles = pl.tiles;
+  a.by_tiles = make_fastdiv(std::max(1, pl.tiles));
   a.lanes = pl.lanes;
   a.rows = pl.rows;
   return a;
 }
 
-int64_t ln_bwd_ws(const mqv_ln_desc* d, const LnPlan& pl) { return align256(pl.bwd_blocks * 2 * d->C * 4); }
+int64_t ln_bwd_ws(const mqv_ln_desc* d, const LnPlan& pl) { return align256(pl.blocks * 2 * d->C * 4); }
 
 // ----------------------------------------------------------- linear layer
 
@@ -432,18 +519,6 @@ mqv_status encode_output(CUtensorMap* map, const void* p, bool f32, const GemmTc
   return encode(map, f32, 4, p, dims, strides, box);
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  done[dev] = e == cudaSuccess;
-  return e;
-}
-
 template <int BN, bool PAIR, bool FAST>
 cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
@@ -522,19 +597,11 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
     const int64_t inner = g.e.bias_on_row ? g.col_inner : 1, channels = g.e.bias_on_row ? pl.M : g.col_inner;
     const int v = g.e.vec4 ? 4 : 1;
     const unsigned blocks = (unsigned)ceil_div(pl.out_elems, 32 * v);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = blocks;
-    cfg.blockDim = 256;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    DependentLaunch l(blocks, 256, st);
     const float* part = g.part;
     const cudaError_t se =
-        v == 4 ? cudaLaunchKernelEx(&cfg, split_sum_kernel<4>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels)
-               : cudaLaunchKernelEx(&cfg, split_sum_kernel<1>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels);
+        v == 4 ? cudaLaunchKernelEx(&l.cfg, split_sum_kernel<4>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels)
+               : cudaLaunchKernelEx(&l.cfg, split_sum_kernel<1>, g.e, part, g.splits, g.part_stride, pl.out_elems, inner, channels);
     if (se != cudaSuccess) return cuda_fail(se, "linear layer launch");
   }
   return launched("linear layer launch");
@@ -553,8 +620,8 @@ extern "C" {
 
 mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const float* gamma, const float* beta,
                       void* y, int32_t y_type, float* mean, float* rstd, void* stream) {
-  LnPlan pl = {};
-  mqv_status st = plan_ln(d, &pl);
+  LnPlan pl;
+  mqv_status st = plan_ln(d, false, &pl);
   if (st || (st = check_type(x_type, "x")) || (st = check_type(y_type, "y"))) return st;
   const int64_t cols = d->P * d->N, n = cols * d->C;
   if (!mean != !rstd) return fail(MQV_ERR_INVALID_ARG, "mean and rstd: both or neither");
@@ -572,13 +639,13 @@ mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const
   a.mean = mean;
   a.rstd = rstd;
   a.out = {y, y_type == MQV_BF16};
-  launch_ln<false>(a, pl, d->N == 1, static_cast<cudaStream_t>(stream));
-  return launched("layer norm launch");
+  const cudaError_t e = launch_ln_fwd(a, pl, d->N == 1, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "layer norm launch");
 }
 
 mqv_status mqv_ln_bwd_workspace_size(const mqv_ln_desc* d, size_t* bytes) {
-  LnPlan pl = {};
-  mqv_status st = plan_ln(d, &pl);
+  LnPlan pl;
+  mqv_status st = plan_ln(d, true, &pl);
   if (st) return st;
   if (!bytes) return fail(MQV_ERR_INVALID_ARG, "null output pointer");
   *bytes = (size_t)ln_bwd_ws(d, pl);
@@ -588,8 +655,8 @@ mqv_status mqv_ln_bwd_workspace_size(const mqv_ln_desc* d, size_t* bytes) {
 mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, const void* x, int32_t x_type,
                       const float* mean, const float* rstd, const float* gamma, void* gx, int32_t gx_type,
                       float* ggamma, float* gbeta, void* ws, size_t ws_bytes, void* stream) {
-  LnPlan pl = {};
-  mqv_status st = plan_ln(d, &pl);
+  LnPlan pl;
+  mqv_status st = plan_ln(d, true, &pl);
   if (st || (st = check_type(gy_type, "gy")) || (st = check_type(x_type, "x")) || (st = check_type(gx_type, "gx")))
     return st;
   const int64_t cols = d->P * d->N, n = cols * d->C;
@@ -614,8 +681,11 @@ mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, con
   a.rstd = const_cast<float*>(rstd);
   a.out = {gx, gx_type == MQV_BF16};
   a.part = ggamma ? static_cast<float*>(ws) : nullptr;
-  if (cols > 0) launch_ln<true>(a, pl, d->N == 1, s);
-  if (ggamma) launch_column_sum(a.part, pl.bwd_blocks, d->C, 2, ggamma, gbeta, s);
+  if (cols > 0) {
+    const cudaError_t e = launch_ln_bwd(a, pl, d->N == 1, s);
+    if (e != cudaSuccess) return cuda_fail(e, "layer norm gradient launch");
+  }
+  if (ggamma) launch_column_sum(a.part, pl.blocks, d->C, 2, ggamma, gbeta, s);
   return launched("layer norm gradient launch");
 }
 

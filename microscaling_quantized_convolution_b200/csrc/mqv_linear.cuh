@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(256) act_grad_row_kernel(const ActGradArgs a) 
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e] += g[e];
     }
+  pdl_launch_dependents();
   if (!a.part) return;
 #pragma unroll
   for (int e = 0; e < V; ++e) s[q][lane * V + e] = acc[e];
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(256) act_grad_tile_kernel(const ActGradArgs a)
       for (int e = 0; e < V; ++e) acc += g[e];
     }
   }
+  pdl_launch_dependents();
   if (!a.part) return;
   s[threadIdx.x] = acc;
   __syncthreads();

@@ -7,22 +7,29 @@
 // Memory-bound: each tensor is read once into registers and written once.
 // The variance is summed around the mean (a second pass over the registers),
 // so a large common offset costs no precision; all sums are fp32.
-//   - Rows (N = 1): a block takes a row at a time, a thread K vectors of V
-//     consecutive channels.
-//   - Columns (N > 1): a block takes the C x TN tile of one position and TN
-//     batch items; a thread K vectors of V batch items, R channels apart, so
-//     a warp's loads are runs of whole tile rows.
-// The backward blocks run over many rows or tiles and keep their channels'
-// parameter gradients in registers; each block writes one partial row, and
-// column_sum_kernel adds the rows in a fixed order.
+//   - Rows (N = 1): a group of threads takes a row at a time, a thread K
+//     vectors of 8 consecutive channels, or E scalars where rows are no whole
+//     number of vectors.
+//   - Tiles (N > 1): a group takes the C x TN tile of one position and TN
+//     batch items; a thread K vectors of 4 batch items (or scalars), `rows`
+//     channels apart, so a warp's loads are runs of whole tile rows.
+// What bounds these kernels besides memory is the number of instructions an
+// element costs: threads hold many elements, so that the reductions' cost is
+// spread, arithmetic is on pairs (fma.rn.f32x2 and its kin: two IEEE
+// operations an instruction), and addresses are stepped, not multiplied.
+// Rows of vectors are on their way, D rows ahead (three, or one where
+// three do not fit), into slots of shared
+// memory that only the thread itself uses: loads stay in flight across the
+// reductions, and no barrier is needed for them.
+// The backward groups run over many rows or tiles and keep their channels'
+// parameter gradients in registers; a block adds its groups' in order and
+// writes one partial row, and column_sum_kernel adds the rows in a fixed order.
 #pragma once
 
 #include "mqv_layer_common.cuh"
+#include "mqv_ptx.cuh"
 
 namespace mqv {
-
-constexpr int kLnMaxThreads = 1024;
-constexpr int kLnFewThreads = 256;   // blocks up to this size may use more registers: the T of the kernels
 
 struct LnArgs {
   int64_t P, N;
@@ -33,309 +40,748 @@ struct LnArgs {
   TensorIn x, gy;
   TensorOut out;               // y, or gx
   float* part;                 // backward: [gridDim.x][2][C]; null: no parameter gradients
-  // columns
+  int group;                   // threads of a group, whole warps
+  int units;                   // rows or tiles
+  // tiles
   int tn, tiles;               // batch items per tile, tiles along the batch
+  FastDiv by_tiles;
   int lanes, rows;             // threads along a tile row, channels per step
 };
 
-// Sum over the block; every thread gets it.  buf: 33 floats.
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-  v = warp_sum(v);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();               // buf free
-  if (lane == 0) buf[w] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? buf[lane] : 0.f);
+// The threads of one group and its barrier.  MANY: a block may hold several
+// groups of more than a warp, each with a barrier of its own (an SM has 64 of
+// them, so such blocks are few); otherwise a group is a warp or the block.
+template <bool MANY>
+struct LnGroup {
+  int size, index, tid;
+  __device__ __forceinline__ explicit LnGroup(int group) : size(group), index(threadIdx.x / group) {
+    tid = threadIdx.x - index * group;
+  }
+  __device__ __forceinline__ void sync() const {
+    if (size == 32)
+      __syncwarp();
+    else if (MANY)
+      asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(size) : "memory");
+    else
+      __syncthreads();
+  }
+};
+
+// M sums over a group; every thread gets them.  buf: 32·M floats of the
+// group's own, not those of the call before.
+template <int M, typename G>
+__device__ __forceinline__ void group_sum(const G& g, float (&v)[M], float* buf) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = warp_sum(v[m]);
+  if (g.size == 32) return;
+  const int w = g.tid >> 5, lane = g.tid & 31, warps = g.size >> 5;
+  if (lane == 0)
+#pragma unroll
+    for (int m = 0; m < M; ++m) buf[32 * m + w] = v[m];
+  g.sync();
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = warp_sum(lane < warps ? buf[32 * m + lane] : 0.f);
 }
 
-template <int V, int K>
-__device__ __forceinline__ void load_row(const TensorIn& t, int64_t base, int C, float (&v)[K][V]) {
-  if (t.bf16) {
+// ------------------------------------------------------- pairs of floats
+
+using pair_t = unsigned long long;
+
+__device__ __forceinline__ pair_t pair(float lo, float hi) {
+  pair_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float hi(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+  pair_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// V elements (8, 4 or 2 scalars `apart` elements from each other) as V / 2
+// pairs; p is their first element.
+template <bool VEC, int V, bool BF>
+__device__ __forceinline__ void load_pairs(const char* p, int64_t apart, bool second, pair_t (&v)[V / 2]) {
+  if constexpr (!VEC) {
+    float e[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C) load_bf16<V>(t.p, base + c, v[k]);
+    for (int i = 0; i < 2; ++i)
+      if (i == 0 || second) {
+        if constexpr (BF)
+          e[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i * apart)) << 16);
+        else
+          e[i] = __ldg(reinterpret_cast<const float*>(p) + i * apart);
+      }
+    v[0] = pair(e[0], e[1]);
+  } else if constexpr (BF) {
+    uint32_t w[V / 2];
+    if constexpr (V == 8) {
+      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+    } else {
+      const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = t.x, w[1] = t.y;
     }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
   } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C) load_f32<V>(t.p, base + c, v[k]);
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[2 * i] = pair(t.x, t.y);
+      v[2 * i + 1] = pair(t.z, t.w);
     }
   }
 }
 
-template <int V, int K, int T>
-__global__ void __launch_bounds__(T) ln_fwd_row_kernel(const LnArgs a) {
-  __shared__ float buf[33];
-  const int C = a.C;
+template <bool VEC, int V, bool BF>
+__device__ __forceinline__ void store_pairs(char* p, int64_t apart, bool second, const pair_t (&v)[V / 2]) {
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (i == 0 || second) {
+        const float e = i ? hi(v[0]) : lo(v[0]);
+        if constexpr (BF)
+          reinterpret_cast<__nv_bfloat16*>(p)[i * apart] = __float2bfloat16_rn(e);
+        else
+          reinterpret_cast<float*>(p)[i * apart] = e;
+      }
+  } else if constexpr (BF) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16(lo(v[i]), hi(v[i]));
+    if constexpr (V == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(lo(v[2 * i]), hi(v[2 * i]), lo(v[2 * i + 1]), hi(v[2 * i + 1]));
+  }
+}
+
+// K vectors, `step` elements apart, those whose bit in `mask` is set (scalars:
+// a bit for each of the two).  The type is tested once, around the loop.
+template <bool VEC, int V, int K>
+__device__ __forceinline__ void load_all(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, pair_t (&v)[K][V / 2]) {
+  const int64_t hop = VEC ? step : 2 * step;
+  if (t.bf16) {
+    const char* p = static_cast<const char*>(t.p) + i * 2;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += hop * 2)
+      if (mask >> (VEC ? k : 2 * k) & 1) load_pairs<VEC, V, true>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+  } else {
+    const char* p = static_cast<const char*>(t.p) + i * 4;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += hop * 4)
+      if (mask >> (VEC ? k : 2 * k) & 1) load_pairs<VEC, V, false>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+  }
+}
+
+template <bool VEC, int V, int K>
+__device__ __forceinline__ void store_all(const TensorOut& t, int64_t i, int64_t step, uint32_t mask,
+                                          const pair_t (&v)[K][V / 2]) {
+  const int64_t hop = VEC ? step : 2 * step;
+  if (t.bf16) {
+    char* p = static_cast<char*>(t.p) + i * 2;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += hop * 2)
+      if (mask >> (VEC ? k : 2 * k) & 1) store_pairs<VEC, V, true>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+  } else {
+    char* p = static_cast<char*>(t.p) + i * 4;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += hop * 4)
+      if (mask >> (VEC ? k : 2 * k) & 1) store_pairs<VEC, V, false>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+  }
+}
+
+// Bits of the `n` items, `step` apart from `first`, that are below `end`.
+__device__ __forceinline__ uint32_t items_below(int first, int step, int n, int end) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < n; ++i) m |= static_cast<uint32_t>(first + i * step < end) << i;
+  return m;
+}
+
+// --------------------------------------------------- prefetched row vectors
+//
+// A thread's K vectors of 8 elements of one tensor, as 16-byte pieces; piece j
+// of the block's thread t lies at (j·blockDim + t)·16 in the tensor's slot.
+
+template <int K>
+__device__ __forceinline__ void slot_fetch(const TensorIn& t, int64_t i, int step, uint32_t mask, uint32_t slot) {
+  const uint32_t hop = blockDim.x * 16;
+  slot += threadIdx.x * 16;
+  if (t.bf16) {
+    const char* p = static_cast<const char*>(t.p) + i * 2;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += step * 2)
+      if (mask >> k & 1) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * hop), "l"(p) : "memory");
+  } else {
+    const char* p = static_cast<const char*>(t.p) + i * 4;
+#pragma unroll
+    for (int k = 0; k < K; ++k, p += step * 4)
+      if (mask >> k & 1) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + 2 * k * hop), "l"(p) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (2 * k + 1) * hop), "l"(p + 16) : "memory");
+      }
+  }
+}
+
+template <int K>
+__device__ __forceinline__ void slot_read(const TensorIn& t, uint32_t mask, uint32_t slot, pair_t (&v)[K][4]) {
+  const uint32_t hop = blockDim.x * 16;
+  slot += threadIdx.x * 16;
+  if (t.bf16) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mask >> k & 1) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(slot + k * hop) : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k][i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mask >> k & 1) {
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[k][0]), "=l"(v[k][1]) : "r"(slot + 2 * k * hop) : "memory");
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[k][2]), "=l"(v[k][3]) : "r"(slot + (2 * k + 1) * hop) : "memory");
+      }
+  }
+}
+
+__device__ __forceinline__ void slot_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest D - 1 groups have arrived.
+template <int D>
+__device__ __forceinline__ void slot_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
+__device__ __forceinline__ void slot_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ------------------------------------------------------------------- rows
+//
+// VEC: K vectors of V = 8 channels a thread, else K pairs of scalars (V = 2).
+
+// D: rows in flight; B: blocks an SM that the registers must allow; KEEP:
+// gamma and beta stay in registers, where there are some left, else they are
+// read again for each row (from L1).
+template <bool VEC, int K, int T, int B, int D, bool KEEP>
+__global__ void __launch_bounds__(T, B) ln_fwd_row_kernel(const LnArgs a) {
+  constexpr int V = VEC ? 8 : 2, kItems = VEC ? K : 2 * K;
+  extern __shared__ __align__(16) uint8_t slots[];
+  __shared__ float bufs[T / 32][2][32];
+  const LnGroup<false> grp(a.group);
+  const int groups = blockDim.x / grp.size;
+  const int C = a.C, step = grp.size * (VEC ? V : 1), c0 = grp.tid * (VEC ? V : 1);
   const float inv = 1.f / C;
-  for (int64_t p = blockIdx.x; p < a.P; p += gridDim.x) {
-    float v[K][V];
-    load_row<V, K>(a.x, p * C, C, v);
-    float s = 0.f;
+  const uint32_t mask = items_below(c0, step, kItems, C);
+  const uint32_t s0 = smem_u32(slots), slot_bytes = K * blockDim.x * (a.x.bf16 ? 16 : 32);
+  const int first = blockIdx.x * groups + grp.index, hop = gridDim.x * groups;
+  auto fetch = [&](int p, uint32_t slot) {
+    if constexpr (VEC) {
+      if (p < a.units) slot_fetch<K>(a.x, static_cast<int64_t>(p) * C + c0, step, mask, slot);
+      slot_commit();
+    }
+  };
+  pair_t gam[K][V / 2], bet[K][V / 2];
+  auto parameters = [&] {
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if ((threadIdx.x + k * blockDim.x) * V < C)
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += v[k][e];
-    const float mean = block_sum(s, buf) * inv;
-    s = 0.f;
+      for (int i = 0; i < V / 2; ++i) {
+        gam[k][i] = pair(1.f, 1.f);
+        bet[k][i] = 0;
+      }
+    if (a.gamma) load_all<VEC, V, K>(TensorIn{a.gamma, 0}, c0, step, mask, gam);
+    if (a.beta) load_all<VEC, V, K>(TensorIn{a.beta, 0}, c0, step, mask, bet);
+  };
+  if constexpr (KEEP) parameters();
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(first + i * hop, s0 + i * slot_bytes);
+  int turn = 0;
+  for (int p = first; p < a.units; p += hop) {
+    const int64_t at = static_cast<int64_t>(p) * C + c0;
+    const uint32_t slot = s0 + turn * slot_bytes;
+    turn = turn + 1 < D ? turn + 1 : 0;
+    pair_t v[K][V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if ((threadIdx.x + k * blockDim.x) * V < C)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          v[k][e] -= mean;
-          s += v[k][e] * v[k][e];
-        }
-    const float rstd = 1.f / sqrtf(block_sum(s, buf) * inv + a.eps);
-    if (threadIdx.x == 0 && a.mean) {
+      for (int i = 0; i < V / 2; ++i) v[k][i] = 0;
+    if constexpr (VEC) {
+      slot_wait<D>();
+      slot_read<K>(a.x, mask, slot, v);
+    } else {
+      load_all<VEC, V, K>(a.x, at, step, mask, v);
+    }
+    pair_t t = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) t = add2(t, v[k][i]);
+    float s[1] = {lo(t) + hi(t)};
+    group_sum(grp, s, bufs[grp.index][0]);
+    fetch(p + D * hop, slot);               // what was there is in registers
+    const float mean = s[0] * inv;
+    const pair_t minus = pair(-mean, -mean);
+    t = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mask >> (VEC ? k : 2 * k) & 1) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v[k][i] = add2(v[k][i], minus);
+        if (!VEC && !(mask >> (2 * k + 1) & 1)) v[k][0] = pair(lo(v[k][0]), 0.f);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) t = fma2(v[k][i], v[k][i], t);
+      }
+    s[0] = lo(t) + hi(t);
+    group_sum(grp, s, bufs[grp.index][1]);
+    const float rstd = rsqrtf(s[0] * inv + a.eps);
+    if (grp.tid == 0 && a.mean) {
       a.mean[p] = mean;
       a.rstd[p] = rstd;
     }
+    const pair_t r2 = pair(rstd, rstd);
+    if constexpr (!KEEP) parameters();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C) {
-        float g[V], b[V];
-        if (a.gamma) load_f32<V>(a.gamma, c, g);
-        if (a.beta) load_f32<V>(a.beta, c, b);
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float y = v[k][e] * rstd;
-          if (a.gamma) y *= g[e];
-          if (a.beta) y += b[e];
-          v[k][e] = y;
-        }
-        store_vec<V>(a.out, p * C + c, v[k]);
-      }
-    }
+      for (int i = 0; i < V / 2; ++i) v[k][i] = fma2(mul2(v[k][i], r2), gam[k][i], bet[k][i]);
+    store_all<VEC, V, K>(a.out, at, step, mask, v);
   }
 }
 
-template <int V, int K, int T>
-__global__ void __launch_bounds__(T) ln_bwd_row_kernel(const LnArgs a) {
-  __shared__ float buf[2][33];
-  const int C = a.C;
+// A block's partial row: the groups' sums of a channel added in their order.
+// `put(acc)` adds the calling thread's own sums to acc[2][C].
+template <typename G, typename F>
+__device__ __forceinline__ void write_partial(const LnArgs& a, const G& grp, int turns, int turn, float* acc, F put) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.C; i += blockDim.x) acc[i] = 0.f;
+  __syncthreads();
+  const int groups = blockDim.x / grp.size;
+  for (int g = 0; g < groups; ++g)
+    for (int t = 0; t < turns; ++t) {
+      if (grp.index == g && turn == t) put(acc);
+      __syncthreads();
+    }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
+  for (int i = threadIdx.x; i < 2 * a.C; i += blockDim.x) part[i] = acc[i];
+}
+
+template <bool VEC, int K, int T, int B, int D>
+__global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
+  constexpr int V = VEC ? 8 : 2, kItems = VEC ? K : 2 * K;
+  extern __shared__ __align__(16) uint8_t slots[];
+  __shared__ float bufs[T / 32][2][64];
+  const LnGroup<true> grp(a.group);
+  const int groups = blockDim.x / grp.size;
+  const int C = a.C, step = grp.size * (VEC ? V : 1), c0 = grp.tid * (VEC ? V : 1);
   const float inv = 1.f / C;
-  float ag[K][V], ab[K][V];
+  const uint32_t mask = items_below(c0, step, kItems, C);
+  const uint32_t s0 = smem_u32(slots), x_bytes = K * blockDim.x * (a.x.bf16 ? 16 : 32);
+  const uint32_t slot_bytes = x_bytes + K * blockDim.x * (a.gy.bf16 ? 16 : 32);
+  const int first = blockIdx.x * groups + grp.index, hop = gridDim.x * groups;
+  auto fetch = [&](int p, uint32_t slot) {
+    if constexpr (VEC) {
+      if (p < a.units) {
+        const int64_t at = static_cast<int64_t>(p) * C + c0;
+        slot_fetch<K>(a.x, at, step, mask, slot);
+        slot_fetch<K>(a.gy, at, step, mask, slot + x_bytes);
+      }
+      slot_commit();
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(first + i * hop, s0 + i * slot_bytes);
+  // ag, ab: sums of gy·xh and gy; gamma comes in again for each row (from L1),
+  // which costs fewer registers than it saves
+  pair_t ag[K][V / 2], ab[K][V / 2];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int e = 0; e < V; ++e) ag[k][e] = ab[k][e] = 0.f;
-  for (int64_t p = blockIdx.x; p < a.P; p += gridDim.x) {
-    float x[K][V], g[K][V];
-    load_row<V, K>(a.x, p * C, C, x);
-    load_row<V, K>(a.gy, p * C, C, g);
-    const float mean = a.mean[p], rstd = a.rstd[p];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C) {
-        float w[V];
-        if (a.gamma) load_f32<V>(a.gamma, c, w);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x[k][e] = (x[k][e] - mean) * rstd;
-          ag[k][e] += g[k][e] * x[k][e];
-          ab[k][e] += g[k][e];
-          if (a.gamma) g[k][e] *= w[e];
-          s1 += g[k][e];
-          s2 += g[k][e] * x[k][e];
-        }
-      }
-    }
-    s1 = block_sum(s1, buf[0]) * inv;
-    s2 = block_sum(s2, buf[1]) * inv;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) g[k][e] = rstd * (g[k][e] - s1 - x[k][e] * s2);
-        store_vec<V>(a.out, p * C + c, g[k]);
-      }
-    }
-  }
-  if (a.part) {
-    float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * C;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (threadIdx.x + k * blockDim.x) * V;
-      if (c < C)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          part[c + e] = ag[k][e];
-          part[C + c + e] = ab[k][e];
-        }
-    }
-  }
-}
-
-// Sums the V values of the threads that share a tile column (same thread
-// index modulo `lanes`) over the block's channel rows; every active thread
-// gets its column's sums.  buf: blockDim.x·V floats.
-template <int V>
-__device__ __forceinline__ void tile_sum(float (&v)[V], int lanes, int rows, float* buf) {
-  const int t = threadIdx.x, r = t / lanes;
-  const bool act = r < rows;
-  __syncthreads();               // buf free
-  if (act)
-#pragma unroll
-    for (int e = 0; e < V; ++e) buf[e * blockDim.x + t] = v[e];
-  for (int n = rows; n > 1;) {
-    const int half = (n + 1) / 2;
-    __syncthreads();
-    if (r < n - half)
-#pragma unroll
-      for (int e = 0; e < V; ++e) buf[e * blockDim.x + t] += buf[e * blockDim.x + t + half * lanes];
-    n = half;
-  }
-  __syncthreads();
-  if (act)
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = buf[e * blockDim.x + t % lanes];
-}
-
-template <int V, int K>
-__device__ __forceinline__ void load_tile(const TensorIn& t, int64_t base, int64_t N, int r, int rows, int C, bool act,
-                                          float (&v)[K][V]) {
-  if (t.bf16) {
+    for (int i = 0; i < V / 2; ++i) ag[k][i] = ab[k][i] = 0;
+  int turn = 0, odd = 0;
+  for (int p = first; p < a.units; p += hop, odd ^= 1) {
+    const int64_t at = static_cast<int64_t>(p) * C + c0;
+    const uint32_t slot = s0 + turn * slot_bytes;
+    turn = turn + 1 < D ? turn + 1 : 0;
+    const float mean = __ldg(a.mean + p), rstd = __ldg(a.rstd + p);
+    pair_t x[K][V / 2], g[K][V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (act && r + k * rows < C) load_bf16<V>(t.p, base + (r + k * rows) * N, v[k]);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) x[k][i] = g[k][i] = 0;
+    if constexpr (VEC) {
+      slot_wait<D>();
+      slot_read<K>(a.x, mask, slot, x);
+      slot_read<K>(a.gy, mask, slot + x_bytes, g);
+    } else {
+      load_all<VEC, V, K>(a.x, at, step, mask, x);
+      load_all<VEC, V, K>(a.gy, at, step, mask, g);
+    }
+    const pair_t minus = pair(-mean, -mean), r2 = pair(rstd, rstd);
+    pair_t t1 = 0, t2 = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        x[k][i] = mul2(add2(x[k][i], minus), r2);          // outside the row: gy is 0
+        ag[k][i] = fma2(g[k][i], x[k][i], ag[k][i]);
+        ab[k][i] = add2(ab[k][i], g[k][i]);
+      }
+    if (a.gamma) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (mask >> (VEC ? k : 2 * k) & 1) {
+          pair_t w[V / 2];
+          load_pairs<VEC, V, false>(reinterpret_cast<const char*>(a.gamma + c0 + (VEC ? k : 2 * k) * step), step,
+                                    mask >> (2 * k + 1) & 1, w);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) g[k][i] = mul2(g[k][i], w[i]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        t1 = add2(t1, g[k][i]);
+        t2 = fma2(g[k][i], x[k][i], t2);
+      }
+    float s[2] = {lo(t1) + hi(t1), lo(t2) + hi(t2)};
+    group_sum(grp, s, bufs[grp.index][odd]);
+    fetch(p + D * hop, slot);
+    const pair_t m1 = pair(-s[0] * inv, -s[0] * inv), m2 = pair(-s[1] * inv, -s[1] * inv);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) g[k][i] = mul2(r2, fma2(x[k][i], m2, add2(g[k][i], m1)));
+    store_all<VEC, V, K>(a.out, at, step, mask, g);
+  }
+  slot_wait_all();
+  pdl_launch_dependents();
+  if (!a.part) return;
+  write_partial(a, grp, 1, 0, reinterpret_cast<float*>(slots), [&](float* acc) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int c = c0 + (VEC ? k * step + e : (2 * k + e) * step);
+        if (c < C) {
+          acc[c] += e & 1 ? hi(ag[k][e / 2]) : lo(ag[k][e / 2]);
+          acc[C + c] += e & 1 ? hi(ab[k][e / 2]) : lo(ab[k][e / 2]);
+        }
+      }
+  });
+}
+
+// ------------------------------------------------------------------ tiles
+//
+// VEC: a thread's items are vectors of V = 4 batch items, else single ones
+// (V = 1, held as half a pair).
+
+template <int M>
+__device__ __forceinline__ void read_floats(const float* p, float (&v)[M]) {
+  if constexpr (M % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < M / 4; ++q) {
+      const float4 f = reinterpret_cast<const float4*>(p)[q];
+      v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (act && r + k * rows < C) load_f32<V>(t.p, base + (r + k * rows) * N, v[k]);
+    for (int m = 0; m < M; ++m) v[m] = p[m];
+  }
+}
+
+// Floats that tile_sum needs for `values` sums a thread: the warps' sums and
+// their totals where the lanes divide a warp, else the threads' sums.
+__host__ __device__ inline bool tile_sum_by_warps(int lanes) { return lanes <= 32 && (lanes & (lanes - 1)) == 0; }
+__host__ __device__ inline int tile_sum_floats(int lanes, int size, int values) {
+  return values * (tile_sum_by_warps(lanes) ? (size / 32 + 1) * lanes : size);
+}
+
+// Sums M values over the threads of a group that share a tile column (same
+// thread index modulo `lanes`); every active thread gets its column's sums.
+// buf: tile_sum_floats of the group's own, not those of the call before.
+template <int M, typename G>
+__device__ __forceinline__ void tile_sum(float (&v)[M], const G& g, int lanes, int rows, float* buf) {
+  if (tile_sum_by_warps(lanes)) {
+    // lanes divide a warp: first over the warp, then over the warps
+    for (int o = 16; o >= lanes; o >>= 1)
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    const int warps = g.size >> 5;
+    if (warps == 1) return;
+    const int w = g.tid >> 5, l = g.tid & 31;
+    if (l < lanes)
+#pragma unroll
+      for (int m = 0; m < M; ++m) buf[(w * lanes + l) * M + m] = v[m];
+    g.sync();
+    const int c = l & (lanes - 1), width = lanes * M;
+    if (warps > 4) {
+      // many warps: each sum by one thread, then read by all
+      float* total = buf + warps * width;
+      for (int i = g.tid; i < width; i += g.size) {
+        float f = 0.f;
+        for (int k = 0; k < warps; ++k) f += buf[k * width + i];
+        total[i] = f;
+      }
+      g.sync();
+      read_floats<M>(total + c * M, v);
+      return;
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] = 0.f;
+    for (int i = 0; i < warps; ++i) {
+      float t[M];
+      read_floats<M>(buf + i * width + c * M, t);
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] += t[m];
+    }
+    return;
+  }
+  const int t = g.tid, r = t / lanes;
+  const bool act = r < rows;
+  if (act)
+#pragma unroll
+    for (int m = 0; m < M; ++m) buf[m * g.size + t] = v[m];
+  for (int n = rows; n > 1;) {
+    const int half = (n + 1) / 2;
+    g.sync();
+    if (r < n - half)
+#pragma unroll
+      for (int m = 0; m < M; ++m) buf[m * g.size + t] += buf[m * g.size + t + half * lanes];
+    n = half;
+  }
+  g.sync();
+  if (act)
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] = buf[m * g.size + t % lanes];
+}
+
+// V values as pairs, and back.
+template <int V>
+__device__ __forceinline__ void spread(const pair_t (&t)[(V + 1) / 2], float (&v)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) v[e] = e & 1 ? hi(t[e / 2]) : lo(t[e / 2]);
+}
+template <int V>
+__device__ __forceinline__ void gather(const float* v, pair_t (&t)[(V + 1) / 2]) {
+#pragma unroll
+  for (int e = 0; e < V; e += 2) t[e / 2] = pair(v[e], e + 1 < V ? v[e + 1] : 0.f);
+}
+
+// K items of V elements, `step` elements apart.
+template <int V, int K>
+__device__ __forceinline__ void load_items(const TensorIn& t, int64_t i, int64_t step, uint32_t mask,
+                                           pair_t (&v)[K][(V + 1) / 2]) {
+  if constexpr (V == 4) {
+    load_all<true, 4, K>(t, i, step, mask, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k, i += step)
+      if (mask >> k & 1) {
+        float f[1];
+        if (t.bf16)
+          load_bf16<1>(t.p, i, f);
+        else
+          load_f32<1>(t.p, i, f);
+        v[k][0] = pair(f[0], 0.f);
+      }
+  }
+}
+template <int V, int K>
+__device__ __forceinline__ void store_items(const TensorOut& t, int64_t i, int64_t step, uint32_t mask,
+                                            const pair_t (&v)[K][(V + 1) / 2]) {
+  if constexpr (V == 4) {
+    store_all<true, 4, K>(t, i, step, mask, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k, i += step)
+      if (mask >> k & 1) store_vec<1>(t, i, {lo(v[k][0])});
   }
 }
 
 template <int V, int K, int T>
 __global__ void __launch_bounds__(T) ln_fwd_tile_kernel(const LnArgs a) {
-  extern __shared__ float buf[];
-  const int C = a.C, r = threadIdx.x / a.lanes, l = threadIdx.x % a.lanes;
+  constexpr int H = (V + 1) / 2;
+  extern __shared__ __align__(16) float sums[];
+  const LnGroup<false> grp(a.group);
+  const int u = blockIdx.x * (blockDim.x / grp.size) + grp.index;
+  if (u >= a.units) return;                        // a whole group
+  const int C = a.C, r = grp.tid / a.lanes, l = grp.tid - r * a.lanes;
   const float inv = 1.f / C;
-  const int64_t total = a.P * a.tiles;
-  for (int64_t s = blockIdx.x; s < total; s += gridDim.x) {
-    const int64_t p = s / a.tiles, n = (s % a.tiles) * a.tn + l * V;
-    const bool act = r < a.rows && n < a.N;
-    const int64_t base = p * C * a.N + n;
-    float v[K][V], m[V], q[V];
-    load_tile<V, K>(a.x, base, a.N, r, a.rows, C, act, v);
+  const int p = fdiv(u, a.by_tiles);
+  const int64_t n = static_cast<int64_t>(u - p * a.tiles) * a.tn + l * V;
+  const int sum_floats = tile_sum_floats(a.lanes, grp.size, V);
+  float* buf = sums + grp.index * 2 * sum_floats;
+  const uint32_t mask = r < a.rows && l * V < a.tn && n < a.N ? items_below(r, a.rows, K, C) : 0;
+  const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n, step = a.rows * a.N;
+  pair_t v[K][H], t[H];
 #pragma unroll
-    for (int e = 0; e < V; ++e) m[e] = q[e] = 0.f;
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (act && r + k * a.rows < C)
+    for (int i = 0; i < H; ++i) v[k][i] = 0;
+  load_items<V, K>(a.x, at, step, mask, v);
+  float m[V], q[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) m[e] += v[k][e];
-    tile_sum<V>(m, a.lanes, a.rows, buf);
+  for (int i = 0; i < H; ++i) t[i] = 0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) m[e] *= inv;
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (act && r + k * a.rows < C)
+    for (int i = 0; i < H; ++i) t[i] = add2(t[i], v[k][i]);
+  spread<V>(t, m);
+  tile_sum<V>(m, grp, a.lanes, a.rows, buf);
+  float minus[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          v[k][e] -= m[e];
-          q[e] += v[k][e] * v[k][e];
-        }
-    tile_sum<V>(q, a.lanes, a.rows, buf);
+  for (int e = 0; e < V; ++e) minus[e] = -(m[e] *= inv);
+  pair_t mp[H];
+  gather<V>(minus, mp);
 #pragma unroll
-    for (int e = 0; e < V; ++e) q[e] = 1.f / sqrtf(q[e] * inv + a.eps);
-    if (act && r == 0 && a.mean)
+  for (int i = 0; i < H; ++i) t[i] = 0;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        a.mean[p * a.N + n + e] = m[e];
-        a.rstd[p * a.N + n + e] = q[e];
+  for (int k = 0; k < K; ++k)
+    if (mask >> k & 1)
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        v[k][i] = add2(v[k][i], mp[i]);
+        t[i] = fma2(v[k][i], v[k][i], t[i]);
       }
+  spread<V>(t, q);
+  tile_sum<V>(q, grp, a.lanes, a.rows, buf + sum_floats);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = r + k * a.rows;
-      if (act && c < C) {
-        const float g = a.gamma ? __ldg(a.gamma + c) : 1.f, b = a.beta ? __ldg(a.beta + c) : 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[k][e] = v[k][e] * q[e] * g + b;
-        store_vec<V>(a.out, base + c * a.N, v[k]);
-      }
-    }
-  }
-}
-
-template <int V, int K, int T>
-__global__ void __launch_bounds__(T) ln_bwd_tile_kernel(const LnArgs a) {
-  extern __shared__ float buf[];
-  const int C = a.C, r = threadIdx.x / a.lanes, l = threadIdx.x % a.lanes;
-  const float inv = 1.f / C;
-  const int64_t total = a.P * a.tiles;
-  float ag[K], ab[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) ag[k] = ab[k] = 0.f;
-  for (int64_t s = blockIdx.x; s < total; s += gridDim.x) {
-    const int64_t p = s / a.tiles, n = (s % a.tiles) * a.tn + l * V;
-    const bool act = r < a.rows && n < a.N;
-    const int64_t base = p * C * a.N + n;
-    float x[K][V], g[K][V], m[V], q[V], s1[V], s2[V];
-    load_tile<V, K>(a.x, base, a.N, r, a.rows, C, act, x);
-    load_tile<V, K>(a.gy, base, a.N, r, a.rows, C, act, g);
+  for (int e = 0; e < V; ++e) q[e] = rsqrtf(q[e] * inv + a.eps);
+  if (mask && r == 0 && a.mean)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      m[e] = act ? a.mean[p * a.N + n + e] : 0.f;
-      q[e] = act ? a.rstd[p * a.N + n + e] : 0.f;
-      s1[e] = s2[e] = 0.f;
+      a.mean[p * a.N + n + e] = m[e];
+      a.rstd[p * a.N + n + e] = q[e];
     }
+  gather<V>(q, mp);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k)
+    if (mask >> k & 1) {
       const int c = r + k * a.rows;
-      if (act && c < C) {
-        const float w = a.gamma ? __ldg(a.gamma + c) : 1.f;
+      const float g = a.gamma ? __ldg(a.gamma + c) : 1.f, b = a.beta ? __ldg(a.beta + c) : 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x[k][e] = (x[k][e] - m[e]) * q[e];
-          ag[k] += g[k][e] * x[k][e];
-          ab[k] += g[k][e];
-          g[k][e] *= w;
-          s1[e] += g[k][e];
-          s2[e] += g[k][e] * x[k][e];
-        }
-      }
+      for (int i = 0; i < H; ++i) v[k][i] = fma2(mul2(v[k][i], mp[i]), pair(g, g), pair(b, b));
     }
-    tile_sum<V>(s1, a.lanes, a.rows, buf);
-    tile_sum<V>(s2, a.lanes, a.rows, buf);
+  store_items<V, K>(a.out, at, step, mask, v);
+}
+
+template <int V, int K, int T, int B>
+__global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
+  constexpr int H = (V + 1) / 2;
+  extern __shared__ __align__(16) float sums[];
+  const LnGroup<true> grp(a.group);
+  const int groups = blockDim.x / grp.size;
+  const int C = a.C, r = grp.tid / a.lanes, l = grp.tid - r * a.lanes;
+  const float inv = 1.f / C;
+  const int64_t step = a.rows * a.N;
+  const int sum_floats = tile_sum_floats(a.lanes, grp.size, 2 * V);
+  float* buf = sums + grp.index * 2 * sum_floats;  // two, used in turn
+  const uint32_t items = r < a.rows && l * V < a.tn ? items_below(r, a.rows, K, C) : 0;
+  float w[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = r + k * a.rows;
-      if (act && c < C) {
+  for (int k = 0; k < K; ++k) w[k] = a.gamma && (items >> k & 1) ? __ldg(a.gamma + r + k * a.rows) : 1.f;
+  pair_t ag[K], ab[K];
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[k][e] = q[e] * (g[k][e] - s1[e] * inv - x[k][e] * (s2[e] * inv));
-        store_vec<V>(a.out, base + c * a.N, g[k]);
-      }
+  for (int k = 0; k < K; ++k) ag[k] = ab[k] = 0;
+  int turn = 0;
+  for (int u = blockIdx.x * groups + grp.index; u < a.units; u += gridDim.x * groups, turn ^= 1) {
+    const int p = fdiv(u, a.by_tiles);
+    const int64_t n = static_cast<int64_t>(u - p * a.tiles) * a.tn + l * V;
+    const uint32_t mask = n < a.N ? items : 0;
+    const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n;
+    pair_t x[K][H], g[K][H], mp[H], qp[H], t1[H], t2[H];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < H; ++i) x[k][i] = g[k][i] = 0;
+    load_items<V, K>(a.x, at, step, mask, x);
+    load_items<V, K>(a.gy, at, step, mask, g);
+    float m[V], q[V];
+    if (mask) {
+      load_f32<V>(a.mean, p * a.N + n, m);
+      load_f32<V>(a.rstd, p * a.N + n, q);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) m[e] = q[e] = 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) m[e] = -m[e];
+    gather<V>(m, mp);
+    gather<V>(q, qp);
+#pragma unroll
+    for (int i = 0; i < H; ++i) t1[i] = t2[i] = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        x[k][i] = mul2(add2(x[k][i], mp[i]), qp[i]);       // outside: gy is 0
+        ag[k] = fma2(g[k][i], x[k][i], ag[k]);
+        ab[k] = add2(ab[k], g[k][i]);
+        g[k][i] = mul2(g[k][i], pair(w[k], w[k]));
+        t1[i] = add2(t1[i], g[k][i]);
+        t2[i] = fma2(g[k][i], x[k][i], t2[i]);
+      }
+    float s[2 * V], s1[V], s2[V];
+    spread<V>(t1, s1);
+    spread<V>(t2, s2);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = s1[e], s[V + e] = s2[e];
+    tile_sum<2 * V>(s, grp, a.lanes, a.rows, buf + turn * sum_floats);
+#pragma unroll
+    for (int e = 0; e < 2 * V; ++e) s[e] *= -inv;
+    gather<V>(s, t1);
+    gather<V>(s + V, t2);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < H; ++i) g[k][i] = mul2(qp[i], fma2(x[k][i], t2[i], add2(g[k][i], t1[i])));
+    store_items<V, K>(a.out, at, step, mask, g);
   }
-  if (a.part) {
-    // a channel's sums over the lanes of its row, added in lane order
-    float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * C;
+  pdl_launch_dependents();
+  if (!a.part) return;
+  // a channel's sums over the lanes of its row, then over the groups
+  float fg[K], fb[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    fg[k] = lo(ag[k]) + hi(ag[k]);
+    fb[k] = lo(ab[k]) + hi(ab[k]);
+  }
+  int turns = a.lanes;
+  if (tile_sum_by_warps(a.lanes)) {
+    for (int o = a.lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        fg[k] += __shfl_xor_sync(0xffffffffu, fg[k], o);
+        fb[k] += __shfl_xor_sync(0xffffffffu, fb[k], o);
+      }
+    turns = 1;
+  }
+  write_partial(a, grp, turns, l, sums, [&](float* acc) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      __syncthreads();
-      buf[threadIdx.x] = ag[k];
-      buf[blockDim.x + threadIdx.x] = ab[k];
-      __syncthreads();
       const int c = r + k * a.rows;
-      if (l < 2 && r < a.rows && c < C) {
-        for (int h = l; h < 2; h += a.lanes) {
-          float t = 0.f;
-          for (int i = 0; i < a.lanes; ++i) t += buf[h * blockDim.x + r * a.lanes + i];
-          part[h * C + c] = t;
-        }
+      if (r < a.rows && c < C) {
+        acc[c] += fg[k];
+        acc[C + c] += fb[k];
       }
     }
-  }
+  });
 }
 
 }  // namespace mqv
