@@ -110,32 +110,12 @@ __device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
   return r;
 }
 
-// V elements (8, 4 or 2 scalars `apart` elements from each other) as V / 2
-// pairs; p is their first element.
-template <bool VEC, int V, bool BF>
-__device__ __forceinline__ void load_pairs(const char* p, int64_t apart, bool second, pair_t (&v)[V / 2]) {
+// V fp32 elements (8, 4 or 2 scalars `apart` elements from each other) as
+// V / 2 pairs; p is their first element.
+template <bool VEC, int V>
+__device__ __forceinline__ void load_pairs(const float* p, int64_t apart, bool second, pair_t (&v)[V / 2]) {
   if constexpr (!VEC) {
-    float e[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (i == 0 || second) {
-        if constexpr (BF)
-          e[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i * apart)) << 16);
-        else
-          e[i] = __ldg(reinterpret_cast<const float*>(p) + i * apart);
-      }
-    v[0] = pair(e[0], e[1]);
-  } else if constexpr (BF) {
-    uint32_t w[V / 2];
-    if constexpr (V == 8) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
-    } else {
-      const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = t.x, w[1] = t.y;
-    }
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) v[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+    v[0] = pair(__ldg(p), second ? __ldg(p + apart) : 0.f);
   } else {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
@@ -173,21 +153,82 @@ __device__ __forceinline__ void store_pairs(char* p, int64_t apart, bool second,
   }
 }
 
-// K vectors, `step` elements apart, those whose bit in `mask` is set (scalars:
-// a bit for each of the two).  The type is tested once, around the loop.
-template <bool VEC, int V, int K>
-__device__ __forceinline__ void load_all(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, pair_t (&v)[K][V / 2]) {
-  const int64_t hop = VEC ? step : 2 * step;
+// K vectors of 8 or 4 elements, `step` elements apart, those whose bit in
+// `mask` is set; zeros for the others.  All loads are issued before the first
+// value is used, and the type is tested once, around them.
+template <int V, int K>
+__device__ __forceinline__ void load_vectors(const TensorIn& t, int64_t i, int64_t step, uint32_t mask,
+                                             pair_t (&v)[K][V / 2]) {
   if (t.bf16) {
     const char* p = static_cast<const char*>(t.p) + i * 2;
+    uint32_t w[K][V / 2];
 #pragma unroll
-    for (int k = 0; k < K; ++k, p += hop * 2)
-      if (mask >> (VEC ? k : 2 * k) & 1) load_pairs<VEC, V, true>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+    for (int k = 0; k < K; ++k, p += step * 2) {
+#pragma unroll
+      for (int q = 0; q < V / 2; ++q) w[k][q] = 0;
+      if (mask >> k & 1) {
+        if constexpr (V == 8) {
+          const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+          w[k][0] = r.x, w[k][1] = r.y, w[k][2] = r.z, w[k][3] = r.w;
+        } else {
+          const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
+          w[k][0] = r.x, w[k][1] = r.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int q = 0; q < V / 2; ++q) v[k][q] = pair(bf16_lo(w[k][q]), bf16_hi(w[k][q]));
   } else {
     const char* p = static_cast<const char*>(t.p) + i * 4;
+    float4 r[K][V / 4];
 #pragma unroll
-    for (int k = 0; k < K; ++k, p += hop * 4)
-      if (mask >> (VEC ? k : 2 * k) & 1) load_pairs<VEC, V, false>(p, step, mask >> (2 * k + 1) & 1, v[k]);
+    for (int k = 0; k < K; ++k, p += step * 4)
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        r[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mask >> k & 1) r[k][q] = __ldg(reinterpret_cast<const float4*>(p) + q);
+      }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        v[k][2 * q] = pair(r[k][q].x, r[k][q].y);
+        v[k][2 * q + 1] = pair(r[k][q].z, r[k][q].w);
+      }
+  }
+}
+
+// n single elements, `step` elements apart, zeros where the bit in `mask` is
+// not set.  The loads are unconditional, of the tensor's first element where
+// there is nothing to load, so that none waits for another.
+template <int n>
+__device__ __forceinline__ void load_scalars(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, float (&f)[n]) {
+  if (t.bf16) {
+    uint16_t h[n];
+#pragma unroll
+    for (int k = 0; k < n; ++k, i += step) h[k] = __ldg(static_cast<const uint16_t*>(t.p) + (mask >> k & 1 ? i : 0));
+#pragma unroll
+    for (int k = 0; k < n; ++k) f[k] = mask >> k & 1 ? __uint_as_float(static_cast<uint32_t>(h[k]) << 16) : 0.f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < n; ++k, i += step) f[k] = __ldg(static_cast<const float*>(t.p) + (mask >> k & 1 ? i : 0));
+#pragma unroll
+    for (int k = 0; k < n; ++k) f[k] = mask >> k & 1 ? f[k] : 0.f;
+  }
+}
+
+// A row thread's K vectors of 8, or 2·K scalars.
+template <bool VEC, int V, int K>
+__device__ __forceinline__ void load_all(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, pair_t (&v)[K][V / 2]) {
+  if constexpr (VEC) {
+    load_vectors<V, K>(t, i, step, mask, v);
+  } else {
+    float f[2 * K];
+    load_scalars<2 * K>(t, i, step, mask, f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k][0] = pair(f[2 * k], f[2 * k + 1]);
   }
 }
 
@@ -446,8 +487,7 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
       for (int k = 0; k < K; ++k)
         if (mask >> (VEC ? k : 2 * k) & 1) {
           pair_t w[V / 2];
-          load_pairs<VEC, V, false>(reinterpret_cast<const char*>(a.gamma + c0 + (VEC ? k : 2 * k) * step), step,
-                                    mask >> (2 * k + 1) & 1, w);
+          load_pairs<VEC, V>(a.gamma + c0 + (VEC ? k : 2 * k) * step, step, mask >> (2 * k + 1) & 1, w);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) g[k][i] = mul2(g[k][i], w[i]);
         }
@@ -588,18 +628,12 @@ template <int V, int K>
 __device__ __forceinline__ void load_items(const TensorIn& t, int64_t i, int64_t step, uint32_t mask,
                                            pair_t (&v)[K][(V + 1) / 2]) {
   if constexpr (V == 4) {
-    load_all<true, 4, K>(t, i, step, mask, v);
+    load_vectors<4, K>(t, i, step, mask, v);
   } else {
+    float f[K];
+    load_scalars<K>(t, i, step, mask, f);
 #pragma unroll
-    for (int k = 0; k < K; ++k, i += step)
-      if (mask >> k & 1) {
-        float f[1];
-        if (t.bf16)
-          load_bf16<1>(t.p, i, f);
-        else
-          load_f32<1>(t.p, i, f);
-        v[k][0] = pair(f[0], 0.f);
-      }
+    for (int k = 0; k < K; ++k) v[k][0] = pair(f[k], 0.f);
   }
 }
 template <int V, int K>
@@ -630,10 +664,6 @@ __global__ void __launch_bounds__(T) ln_fwd_tile_kernel(const LnArgs a) {
   const uint32_t mask = r < a.rows && l * V < a.tn && n < a.N ? items_below(r, a.rows, K, C) : 0;
   const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n, step = a.rows * a.N;
   pair_t v[K][H], t[H];
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < H; ++i) v[k][i] = 0;
   load_items<V, K>(a.x, at, step, mask, v);
   float m[V], q[V];
 #pragma unroll
@@ -706,10 +736,6 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
     const uint32_t mask = n < a.N ? items : 0;
     const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n;
     pair_t x[K][H], g[K][H], mp[H], qp[H], t1[H], t2[H];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < H; ++i) x[k][i] = g[k][i] = 0;
     load_items<V, K>(a.x, at, step, mask, x);
     load_items<V, K>(a.gy, at, step, mask, g);
     float m[V], q[V];
