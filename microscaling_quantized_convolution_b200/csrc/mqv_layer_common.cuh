@@ -30,6 +30,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two floats in a 64-bit register, and operations on both at once.
+using pair_t = unsigned long long;
+
+__device__ __forceinline__ pair_t pair(float lo, float hi) {
+  pair_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float lo(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float hi(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+  pair_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // V consecutive elements at element offset i; V·size bytes aligned.
 template <int V>
 __device__ __forceinline__ void load_f32(const void* p, int64_t i, float (&v)[V]) {
@@ -87,9 +113,10 @@ __device__ __forceinline__ void store_vec(const TensorOut& t, int64_t i, const f
                                                 pack_bf16(v[6], v[7]));
     else if constexpr (V == 4)
       *reinterpret_cast<uint2*>(h) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    else
+    else {
 #pragma unroll
       for (int q = 0; q < V; ++q) h[q] = __bfloat16_as_ushort(__float2bfloat16_rn(v[q]));
+    }
   } else {
     float* f = static_cast<float*>(t.p) + i;
     if constexpr (V % 4 == 0) {

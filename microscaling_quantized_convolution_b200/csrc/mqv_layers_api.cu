@@ -294,14 +294,14 @@ mqv_status check_lin(const mqv_lin_desc* d) {
 }
 
 struct ActGradPlan {
-  int v, lanes, rows;
-  int64_t tiles;
+  int v, lanes, rows, tiles;
   unsigned gx, gy;
 };
 
 ActGradPlan plan_act_grad(const mqv_lin_desc* d) {
   ActGradPlan pl = {};
   int64_t steps;
+  pl.tiles = 1;
   if (d->N == 1) {
     pl.v = d->Cout % 8 == 0 ? 8 : 1;
     pl.gx = (unsigned)ceil_div(d->Cout, 32 * pl.v);
@@ -310,14 +310,58 @@ ActGradPlan plan_act_grad(const mqv_lin_desc* d) {
     pl.v = d->N % 8 == 0 ? 8 : d->N % 4 == 0 ? 4 : 1;
     pl.lanes = (int)std::min<int64_t>(ceil_div(d->N, pl.v), 256);
     pl.rows = 256 / pl.lanes;
-    pl.tiles = ceil_div(d->N, (int64_t)pl.lanes * pl.v);
-    pl.gx = (unsigned)ceil_div(d->Cout, pl.rows);
-    steps = d->P * pl.tiles;
+    pl.tiles = (int)ceil_div(d->N, (int64_t)pl.lanes * pl.v);
+    pl.gx = (unsigned)(ceil_div(d->Cout, pl.rows) * pl.tiles);
+    steps = d->P;
   }
   // about eight blocks an SM, four steps a block at least
   const int64_t want = std::max<int64_t>(1, kSms * 8 / pl.gx);
   pl.gy = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(steps, 4)));
   return pl;
+}
+
+template <int V, bool TOKENS>
+cudaError_t launch_act_grad_v(const ActGradArgs& a, int act, dim3 grid, cudaStream_t st) {
+  switch (act) {
+    case MQV_ACT_RELU: act_grad_kernel<V, kActRelu, TOKENS><<<grid, 256, 0, st>>>(a); break;
+    case MQV_ACT_GELU: act_grad_kernel<V, kActGelu, TOKENS><<<grid, 256, 0, st>>>(a); break;
+    case MQV_ACT_SILU: act_grad_kernel<V, kActSilu, TOKENS><<<grid, 256, 0, st>>>(a); break;
+    default: act_grad_kernel<V, kActNone, TOKENS><<<grid, 256, 0, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act_grad(const ActGradArgs& a, const ActGradPlan& pl, int act, cudaStream_t st) {
+  const dim3 grid(pl.gx, pl.gy);
+  if (a.N == 1)
+    return pl.v == 8 ? launch_act_grad_v<8, true>(a, act, grid, st) : launch_act_grad_v<1, true>(a, act, grid, st);
+  if (pl.v == 8) return launch_act_grad_v<8, false>(a, act, grid, st);
+  return pl.v == 4 ? launch_act_grad_v<4, false>(a, act, grid, st) : launch_act_grad_v<1, false>(a, act, grid, st);
+}
+
+// A few tokens: the forward pass reads the weights once, without tiles.
+// (4096 -> 4096, us: 1 token 8 against 27 in 128 x 128 tiles, K split four ways.)
+bool few_tokens(const mqv_lin_desc* d, int op) { return op == MQV_OP_FWD && d->N == 1 && d->P <= kFewTokens; }
+
+template <int P, bool ODD>
+cudaError_t launch_few_tokens_p(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, cudaStream_t st) {
+  constexpr int R = P <= 2 ? 1 : 2;                // rows a warp, which share the tokens' loads
+  // warps to a row, so that a lane's eight loads at a time are all it has
+  int split = 1;
+  while (split < kFewThreads / 32 && d->Cin > split * 256 * (8 / R)) split *= 2;
+  few_tokens_kernel<P, R, ODD><<<(unsigned)ceil_div(d->Cout, R * (kFewThreads / 32 / split)), kFewThreads, 0, st>>>(
+      e, static_cast<const uint16_t*>(w), static_cast<const uint16_t*>(x), (int)d->Cin, (int)d->Cout, split);
+  return cudaGetLastError();
+}
+
+template <bool ODD>
+cudaError_t launch_few_tokens(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, cudaStream_t st) {
+  switch (d->P) {
+    case 1: return launch_few_tokens_p<1, ODD>(d, e, w, x, st);
+    case 2: return launch_few_tokens_p<2, ODD>(d, e, w, x, st);
+    case 3: return launch_few_tokens_p<3, ODD>(d, e, w, x, st);
+    default: return launch_few_tokens_p<4, ODD>(d, e, w, x, st);
+  }
 }
 
 // ---- products on the tensor cores
@@ -550,9 +594,11 @@ cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t s
 // Copies an operand whose rows are unaligned; *p then points at the copy.
 void repitch(const GemmView& v, const void** p, char** ws, cudaStream_t st) {
   if (!v.copied()) return;
-  const int64_t rows = v.pos * v.mid, units = rows * (v.pitch() / 8);
-  repitch_kernel<<<(unsigned)std::min<int64_t>(ceil_div(units, 256), kSms * 16), 256, 0, st>>>(
-      static_cast<const uint16_t*>(*p), reinterpret_cast<uint16_t*>(*ws), rows, (int)v.inner, (int)v.pitch());
+  const int64_t rows = v.pos * v.mid;
+  int per = 1;
+  while (per < 32 && per * 8 < v.inner) per *= 2;
+  repitch_kernel<<<(unsigned)std::min<int64_t>(ceil_div(rows, 256 / per), kSms * 32), 256, 0, st>>>(
+      static_cast<const uint16_t*>(*p), reinterpret_cast<uint16_t*>(*ws), rows, (int)v.inner, (int)v.pitch(), per);
   *p = *ws;
   *ws += v.copy_bytes();
 }
@@ -608,7 +654,11 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
 }
 
 int64_t lin_ws(const mqv_lin_desc* d, int op) {
-  if (op == MQV_OP_ACT_GRAD) return align256((int64_t)plan_act_grad(d).gy * d->Cout * 4);
+  if (op == MQV_OP_ACT_GRAD) {
+    const ActGradPlan pl = plan_act_grad(d);
+    return align256((int64_t)pl.gy * pl.tiles * d->Cout * 4);
+  }
+  if (few_tokens(d, op)) return 0;
   GemmPlan pl;
   plan_gemm(d, op, &pl);
   return pl.out_elems && pl.args.kblocks ? pl.ws_bytes : 0;
@@ -720,6 +770,11 @@ mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, cons
   e.residual = residual;
   e.bias = bias;
   e.act = d->act;
+  if (few_tokens(d, MQV_OP_FWD) && cols > 0) {
+    const cudaError_t ce = d->Cin % 8 == 0 ? launch_few_tokens<false>(d, e, w, x, static_cast<cudaStream_t>(stream))
+                                           : launch_few_tokens<true>(d, e, w, x, static_cast<cudaStream_t>(stream));
+    return ce == cudaSuccess ? ok() : cuda_fail(ce, "linear layer launch");
+  }
   return run_gemm(d, MQV_OP_FWD, d->N == 1 ? x : w, d->N == 1 ? w : x, e, ws, static_cast<cudaStream_t>(stream));
 }
 
@@ -749,27 +804,14 @@ mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_ty
   a.P = d->P;
   a.N = d->N;
   a.C = (int)d->Cout;
-  a.act = d->act;
   a.lanes = pl.lanes;
   a.rows = pl.rows;
   a.tiles = pl.tiles;
-  const dim3 grid(pl.gx, pl.gy);
   if (cols > 0) {
-    if (d->N == 1) {
-      if (pl.v == 8)
-        act_grad_row_kernel<8><<<grid, 256, 0, s>>>(a);
-      else
-        act_grad_row_kernel<1><<<grid, 256, 0, s>>>(a);
-    } else {
-      if (pl.v == 8)
-        act_grad_tile_kernel<8><<<grid, 256, 0, s>>>(a);
-      else if (pl.v == 4)
-        act_grad_tile_kernel<4><<<grid, 256, 0, s>>>(a);
-      else
-        act_grad_tile_kernel<1><<<grid, 256, 0, s>>>(a);
-    }
+    const cudaError_t e = launch_act_grad(a, pl, d->act, s);
+    if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
   }
-  if (gbias) launch_column_sum(a.part, cols > 0 ? pl.gy : 0, d->Cout, 1, gbias, nullptr, s);
+  if (gbias) launch_column_sum(a.part, cols > 0 ? (int64_t)pl.gy * pl.tiles : 0, d->Cout, 1, gbias, nullptr, s);
   return launched("activation gradient launch");
 }
 

@@ -13,70 +13,88 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ pair_t exp2_pair(pair_t x) { return pair(exp2_approx(lo(x)), exp2_approx(hi(x))); }
+__device__ __forceinline__ pair_t rcp_pair(pair_t x) { return pair(rcp_approx(lo(x)), rcp_approx(hi(x))); }
+__device__ __forceinline__ pair_t both(float x) { return pair(x, x); }
 
-// Phi(z), the normal distribution function, and phi = exp(-z^2 / 2).
+// Phi(z), the normal distribution function, and exp(-z^2 / 2), of two values.
 // erf by Hastings' approximation (Abramowitz and Stegun 7.1.26): with t =
 // 1 / (1 + 0.3275911·x), x = |z| / sqrt 2, 1 - erf(x) = t·poly4(t)·exp(-x^2)
 // within 1.5e-7, 0.75e-7 of Phi: less than two roundings of 1 + erf.  Two
-// special-function operations and about a dozen multiply-adds a value; the
+// special-function operations and a dozen other instructions a value; the
 // library's erff costs three times that, more than the products of a tile
 // with 1024 channels.
-__device__ __forceinline__ float normal_cdf(float z, float* phi) {
-  const float t = __fdividef(1.f, fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.f));
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  const float e = exp2_approx(z * z * -0.72134752f);       // -log2(e) / 2
+__device__ __forceinline__ pair_t normal_cdf(pair_t z, pair_t* phi) {
+  const pair_t x = pair(fabsf(lo(z)), fabsf(hi(z)));
+  const pair_t t = rcp_pair(fma2(x, both(0.3275911f * 0.70710678f), both(1.f)));
+  pair_t q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  q = fma2(t, q, both(0.5f * 1.421413741f));
+  q = fma2(t, q, both(0.5f * -0.284496736f));
+  q = fma2(t, q, both(0.5f * 0.254829592f));
+  const pair_t e = exp2_pair(mul2(mul2(z, z), both(-0.72134752f)));      // -log2(e) / 2
   *phi = e;
-  const float tail = 0.5f * t * q * e;
-  return z < 0.f ? tail : 1.f - tail;
+  const pair_t tail = mul2(mul2(t, q), e), body = fma2(tail, both(-1.f), both(1.f));
+  return pair(lo(z) < 0.f ? lo(tail) : lo(body), hi(z) < 0.f ? hi(tail) : hi(body));
 }
 
 // 1 / (1 + exp(-z)); exp overflows to infinity for z < -88, where the result is 0.
-__device__ __forceinline__ float sigmoid(float z) {
-  return __fdividef(1.f, 1.f + exp2_approx(z * -1.44269504f));
+__device__ __forceinline__ pair_t sigmoid(pair_t z) {
+  return rcp_pair(add2(exp2_pair(mul2(z, both(-1.44269504f))), both(1.f)));
 }
 
-__device__ __forceinline__ float act_value(float z, int act) {
-  float phi;
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;       // a NaN stays one
-    case kActGelu: return z * normal_cdf(z, &phi);
-    case kActSilu: return z * sigmoid(z);
-    default: return z;
+template <int ACT>
+__device__ __forceinline__ pair_t act_pair(pair_t z) {
+  if constexpr (ACT == kActGelu) {
+    pair_t phi;
+    return mul2(z, normal_cdf(z, &phi));
+  } else if constexpr (ACT == kActSilu) {
+    return mul2(z, sigmoid(z));
+  } else if constexpr (ACT == kActRelu) {
+    return pair(lo(z) < 0.f ? 0.f : lo(z), hi(z) < 0.f ? 0.f : hi(z));   // a NaN stays one
+  } else {
+    return z;
   }
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu: {
-      float phi;
-      const float c = normal_cdf(z, &phi);
-      return fmaf(z * 0.39894228f, phi, c);
-    }
-    case kActSilu: {
-      const float s = sigmoid(z);
-      return s * fmaf(z, 1.f - s, 1.f);
-    }
-    default: return 1.f;
+template <int ACT>
+__device__ __forceinline__ pair_t slope_pair(pair_t z) {
+  if constexpr (ACT == kActGelu) {
+    pair_t phi;
+    const pair_t c = normal_cdf(z, &phi);
+    return fma2(mul2(z, both(0.39894228f)), phi, c);
+  } else if constexpr (ACT == kActSilu) {
+    const pair_t s = sigmoid(z);
+    return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+  } else if constexpr (ACT == kActRelu) {
+    return pair(lo(z) > 0.f ? 1.f : 0.f, hi(z) > 0.f ? 1.f : 0.f);
+  } else {
+    return both(1.f);
   }
 }
 
 // The activation of K values, its kind tested once.
+template <int ACT, int K>
+__device__ __forceinline__ void act_all(float (&v)[K]) {
+#pragma unroll
+  for (int i = 0; i < K; i += 2) {
+    const pair_t y = act_pair<ACT>(pair(v[i], i + 1 < K ? v[i + 1] : 0.f));
+    v[i] = lo(y);
+    if (i + 1 < K) v[i + 1] = hi(y);
+  }
+}
 template <int K>
 __device__ __forceinline__ void act_values(float (&v)[K], int act) {
-  if (act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActGelu);
-  } else if (act == kActSilu) {
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActSilu);
-  } else if (act == kActRelu) {
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = act_value(v[i], kActRelu);
-  }
+  if (act == kActGelu)
+    act_all<kActGelu>(v);
+  else if (act == kActSilu)
+    act_all<kActSilu>(v);
+  else if (act == kActRelu)
+    act_all<kActRelu>(v);
 }
 
 // What becomes of a sum: y = act(sum + bias) + residual, z = sum + bias kept.
@@ -104,9 +122,7 @@ __device__ __forceinline__ void epilogue_store(const Epilogue& e, int64_t off, i
     }
   }
   if (e.z.p) store_vec<V>(e.z, off, v);
-  if (e.act != kActNone)
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_value(v[i], e.act);
+  act_values(v, e.act);
   if (e.residual) {
     // a plain load: the residual may be the output buffer itself
     float r[V];

@@ -83,32 +83,7 @@ __device__ __forceinline__ void group_sum(const G& g, float (&v)[M], float* buf)
   for (int m = 0; m < M; ++m) v[m] = warp_sum(lane < warps ? buf[32 * m + lane] : 0.f);
 }
 
-// ------------------------------------------------------- pairs of floats
-
-using pair_t = unsigned long long;
-
-__device__ __forceinline__ pair_t pair(float lo, float hi) {
-  pair_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float lo(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
-__device__ __forceinline__ float hi(pair_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
-__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
-  pair_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
-  pair_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
-  pair_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+// ------------------------------------------------------- vectors as pairs
 
 // V fp32 elements (8, 4 or 2 scalars `apart` elements from each other) as
 // V / 2 pairs; p is their first element.
