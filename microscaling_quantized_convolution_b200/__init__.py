@@ -643,79 +643,99 @@ def dw_wgrad(d: DwDesc, gy: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | No
 # stream, so their memory is not handed out again before the stream is done
 # with it.
 
-_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+# The checks are written to cost little when all is well: the smallest of these
+# calls take less time on the device than a handful of property look-ups here.
+
+_F32, _BF16 = torch.float32, torch.bfloat16
+_TYPES = {_F32: 0, _BF16: 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _OnDevice:
-    """Makes `device` (and `stream`, if one is given) current for a call and
-    holds the stream's handle.  The common case, the current device and no
-    stream given, costs two look-ups."""
-    __slots__ = ("handle", "_dev", "_ctx")
+class _OnStream:
+    """Makes `stream` and its device current, or the device `index` where that
+    is not the current one."""
+    __slots__ = ("_ctx",)
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self._dev = self._ctx = None
+    def __init__(self, index, stream):
         if stream is not None:
+            if stream.device_index != index:
+                raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{index}")
             self._ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self._dev = torch.cuda.device(device)
+        else:
+            self._ctx = torch.cuda.device(index)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        elif self._dev is not None:
-            self._dev.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
+        self._ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        elif self._dev is not None:
-            self._dev.__exit__(*exc)
+        self._ctx.__exit__(*exc)
 
 
-def _operand(t, name: str, n: int, device, dtype=None):
-    """Checks a tensor of n elements on `device`: the C ABI takes no tensor
-    sizes, so a short tensor would be read or written out of bounds there."""
-    if not t.is_cuda:
+class _Current:
+    """The usual case: nothing to make current."""
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_CURRENT = _Current()
+
+
+def _on(index, stream):
+    if stream is None and torch.cuda.current_device() == index:
+        return _CURRENT
+    return _OnStream(index, stream)
+
+
+def _device_of(t, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    return index
+
+
+def _operand(t, name: str, n: int, index: int, dtype=None):
+    """The pointer of a tensor of n elements on device `index`: the C ABI takes
+    no tensor sizes, so a short tensor would be read or written out of bounds."""
+    if t.get_device() == index and t.numel() == n and t.is_contiguous() and \
+            (t.dtype is dtype if dtype is not None else t.dtype in _TYPES):
+        return t.data_ptr()
+    if _device_of(t, name) != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is None:
-        if t.dtype not in _TYPES:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    elif t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} elements, the descriptor needs {n}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
 
 
-def _optional(t, name: str, n: int, device, dtype=None):
-    return None if t is None else _operand(t, name, n, device, dtype)
-
-
-def _result(t, name: str, shape, dtype, device):
-    """(tensor, pointer) of an output: `t` checked, or a new tensor."""
-    if t is None:
-        if dtype not in _TYPES:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr()
-    n = 1
-    for s in shape:
-        n *= s
-    return t, _operand(t, name, n, device, dtype)
+def _result(t, name: str, shape, n: int, dtype, device):
+    """An output: `t` checked, or a new tensor (empty_strided returns sooner than empty)."""
+    if t is not None:
+        _operand(t, name, n, device.index, dtype)
+        return t
+    if dtype not in _TYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    if len(shape) == 3:
+        strides = (shape[1] * shape[2], shape[2], 1)
+    elif len(shape) == 2:
+        strides = (shape[1], 1)
+    else:
+        strides = (1,)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _layer_ws(ws, need: int, device):
+    """(tensor, pointer, bytes) of a workspace: `ws` checked, or a new one."""
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        if not need:
+            return None, None, 0
+        return (t := torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)), t.data_ptr(), need
+    if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -732,26 +752,36 @@ def ln_bwd_workspace_bytes(d: LnDesc) -> int:
     return b.value
 
 
+def _ln_dims(d: LnDesc):
+    P, C, N = d.P, d.C, d.N
+    if P < 0 or C <= 0 or N <= 0:
+        ln_bwd_workspace_bytes(d)        # raises the library's own message
+    return P, C, N
+
+
 def ln_fwd(d: LnDesc, x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
            y: torch.Tensor | None = None, y_dtype=None, mean: torch.Tensor | None = None,
            rstd: torch.Tensor | None = None, stats: bool = True, stream=None):
     """(y, mean, rstd): the layer norm of x [P][C][N] (see mqv_ln_fwd).  y is
     of y_dtype (x's type if not given); mean and rstd [P][N] fp32 are kept for
     ln_bwd, or None with stats=False.  gamma, beta: fp32 [C] or None."""
-    ln_bwd_workspace_bytes(d)
-    dev = x.device
-    n, cols = d.P * d.C * d.N, d.P * d.N
+    P, C, N = _ln_dims(d)
+    dev, at = _device_of(x, "x"), x.device
+    n, cols = P * C * N, P * N
     xp = _operand(x, "x", n, dev)
-    gp, bp = _optional(gamma, "gamma", d.C, dev, torch.float32), _optional(beta, "beta", d.C, dev, torch.float32)
-    with _OnDevice(dev, stream) as on:
-        if y is not None and y_dtype is None:
-            y_dtype = y.dtype
-        y, yp = _result(y, "y", (d.P, d.C, d.N), y_dtype or x.dtype, dev)
+    gp = None if gamma is None else _operand(gamma, "gamma", C, dev, _F32)
+    bp = None if beta is None else _operand(beta, "beta", C, dev, _F32)
+    with _on(dev, stream):
+        if y_dtype is None:
+            y_dtype = x.dtype if y is None else y.dtype
+        y = _result(y, "y", (P, C, N), n, y_dtype, at)
         mp = rp = None
         if stats or mean is not None or rstd is not None:
-            mean, mp = _result(mean, "mean", (d.P, d.N), torch.float32, dev)
-            rstd, rp = _result(rstd, "rstd", (d.P, d.N), torch.float32, dev)
-        _check(lib().mqv_ln_fwd(ctypes.byref(d), xp, _TYPES[x.dtype], gp, bp, yp, _TYPES[y.dtype], mp, rp, on.handle))
+            mean = _result(mean, "mean", (P, N), cols, _F32, at)
+            rstd = _result(rstd, "rstd", (P, N), cols, _F32, at)
+            mp, rp = mean.data_ptr(), rstd.data_ptr()
+        _check(lib().mqv_ln_fwd(ctypes.byref(d), xp, _TYPES[x.dtype], gp, bp, y.data_ptr(), _TYPES[y.dtype], mp, rp,
+                                _raw_stream(dev)))
     return y, mean, rstd
 
 
@@ -761,25 +791,25 @@ def ln_bwd(d: LnDesc, gy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
            ws: torch.Tensor | None = None, stream=None):
     """(gx, ggamma, gbeta) of ln_fwd (see mqv_ln_bwd); gx is of gx_dtype (x's
     type if not given), ggamma and gbeta fp32 [C], None with param_grads=False."""
-    need = ln_bwd_workspace_bytes(d)
-    dev = x.device
-    n, cols = d.P * d.C * d.N, d.P * d.N
+    P, C, N = _ln_dims(d)
+    dev, at = _device_of(x, "x"), x.device
+    n, cols = P * C * N, P * N
     gyp, xp = _operand(gy, "gy", n, dev), _operand(x, "x", n, dev)
-    mp = _operand(mean, "mean", cols, dev, torch.float32)
-    rp = _operand(rstd, "rstd", cols, dev, torch.float32)
-    gp = _optional(gamma, "gamma", d.C, dev, torch.float32)
-    with _OnDevice(dev, stream) as on:
-        if gx is not None and gx_dtype is None:
-            gx_dtype = gx.dtype
-        gx, gxp = _result(gx, "gx", (d.P, d.C, d.N), gx_dtype or x.dtype, dev)
+    mp, rp = _operand(mean, "mean", cols, dev, _F32), _operand(rstd, "rstd", cols, dev, _F32)
+    gp = None if gamma is None else _operand(gamma, "gamma", C, dev, _F32)
+    with _on(dev, stream):
+        if gx_dtype is None:
+            gx_dtype = x.dtype if gx is None else gx.dtype
+        gx = _result(gx, "gx", (P, C, N), n, gx_dtype, at)
         ggp = gbp = wp = None
         wn = 0
         if param_grads or ggamma is not None or gbeta is not None:
-            ggamma, ggp = _result(ggamma, "ggamma", (d.C,), torch.float32, dev)
-            gbeta, gbp = _result(gbeta, "gbeta", (d.C,), torch.float32, dev)
-            ws, wp, wn = _layer_ws(ws, need, dev)
-        _check(lib().mqv_ln_bwd(ctypes.byref(d), gyp, _TYPES[gy.dtype], xp, _TYPES[x.dtype], mp, rp, gp, gxp,
-                                _TYPES[gx.dtype], ggp, gbp, wp, wn, on.handle))
+            ggamma = _result(ggamma, "ggamma", (C,), C, _F32, at)
+            gbeta = _result(gbeta, "gbeta", (C,), C, _F32, at)
+            ggp, gbp = ggamma.data_ptr(), gbeta.data_ptr()
+            ws, wp, wn = _layer_ws(ws, ln_bwd_workspace_bytes(d), at)
+        _check(lib().mqv_ln_bwd(ctypes.byref(d), gyp, _TYPES[gy.dtype], xp, _TYPES[x.dtype], mp, rp, gp, gx.data_ptr(),
+                                _TYPES[gx.dtype], ggp, gbp, wp, wn, _raw_stream(dev)))
     return gx, ggamma, gbeta
 
 
@@ -805,22 +835,22 @@ def lin_fwd(d: LinDesc, w: torch.Tensor, x: torch.Tensor, bias: torch.Tensor | N
     given); z, the bfloat16 pre-activation that lin_act_grad takes, with
     save_z=True (or into the z given), else None.  w: bfloat16 [Cout][Cin]."""
     need = lin_workspace_bytes(d, OP_FWD)
-    dev = x.device
-    n = d.P * d.Cout * d.N
-    wtp = _operand(w, "w", d.Cout * d.Cin, dev, torch.bfloat16)
-    xp = _operand(x, "x", d.P * d.Cin * d.N, dev, torch.bfloat16)
-    bp = _optional(bias, "bias", d.Cout, dev, torch.float32)
+    P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    dev, at = _device_of(x, "x"), x.device
+    n = P * Cout * N
+    wtp = _operand(w, "w", Cout * Cin, dev, _BF16)
+    xp = _operand(x, "x", P * Cin * N, dev, _BF16)
+    bp = None if bias is None else _operand(bias, "bias", Cout, dev, _F32)
     if y_dtype is None:
-        y_dtype = y.dtype if y is not None else residual.dtype if residual is not None else torch.bfloat16
-    rp = _optional(residual, "residual", n, dev, y_dtype)
-    with _OnDevice(dev, stream) as on:
-        shape = (d.P, d.Cout, d.N)
-        y, yp = _result(y, "y", shape, y_dtype, dev)
-        zp = None
+        y_dtype = y.dtype if y is not None else residual.dtype if residual is not None else _BF16
+    rp = None if residual is None else _operand(residual, "residual", n, dev, y_dtype)
+    with _on(dev, stream):
+        y = _result(y, "y", (P, Cout, N), n, y_dtype, at)
         if save_z or z is not None:
-            z, zp = _result(z, "z", shape, torch.bfloat16, dev)
-        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
-        _check(lib().mqv_lin_fwd(ctypes.byref(d), wtp, xp, bp, rp, zp, yp, _TYPES[y.dtype], wp, wn, on.handle))
+            z = _result(z, "z", (P, Cout, N), n, _BF16, at)
+        ws, wp, wn = _layer_ws(ws, need, at)
+        _check(lib().mqv_lin_fwd(ctypes.byref(d), wtp, xp, bp, rp, None if z is None else z.data_ptr(), y.data_ptr(),
+                                 _TYPES[y.dtype], wp, wn, _raw_stream(dev)))
     return y, z
 
 
@@ -831,27 +861,30 @@ def lin_act_grad(d: LinDesc, gy: torch.Tensor, z: torch.Tensor | None = None, gz
     columns, gbias [Cout] (None with bias_grad=False; see mqv_lin_act_grad).
     With act "none", a bfloat16 gy and no gz given, gz is gy itself."""
     need = lin_workspace_bytes(d, OP_ACT_GRAD)
-    dev = gy.device
-    n = d.P * d.Cout * d.N
+    P, Cout, N = d.P, d.Cout, d.N
+    dev, at = _device_of(gy, "gy"), gy.device
+    n = P * Cout * N
     gyp = _operand(gy, "gy", n, dev)
     zp = None
     if d.act != ACT_NONE:
         if z is None:
             raise ValueError("z, the pre-activation that lin_fwd kept, is needed for this activation")
-        zp = _operand(z, "z", n, dev, torch.bfloat16)
-    bias_grad = bias_grad or gbias is not None
-    with _OnDevice(dev, stream) as on:
+        zp = _operand(z, "z", n, dev, _BF16)
+    with _on(dev, stream):
         gzp = gbp = wp = None
         wn = 0
-        if d.act == ACT_NONE and gz is None and gy.dtype == torch.bfloat16:
+        if d.act == ACT_NONE and gz is None and gy.dtype is _BF16:
             gz = gy
         else:
-            gz, gzp = _result(gz, "gz", (d.P, d.Cout, d.N), torch.bfloat16, dev)
-        if bias_grad:
-            gbias, gbp = _result(gbias, "gbias", (d.Cout,), torch.float32, dev)
-            ws, wp, wn = _layer_ws(ws, need, dev)
+            gz = _result(gz, "gz", (P, Cout, N), n, _BF16, at)
+            gzp = gz.data_ptr()
+        if bias_grad or gbias is not None:
+            gbias = _result(gbias, "gbias", (Cout,), Cout, _F32, at)
+            gbp = gbias.data_ptr()
+            ws, wp, wn = _layer_ws(ws, need, at)
         if gzp is not None or gbp is not None:
-            _check(lib().mqv_lin_act_grad(ctypes.byref(d), gyp, _TYPES[gy.dtype], zp, gzp, gbp, wp, wn, on.handle))
+            _check(lib().mqv_lin_act_grad(ctypes.byref(d), gyp, _TYPES[gy.dtype], zp, gzp, gbp, wp, wn,
+                                          _raw_stream(dev)))
     return gz, gbias
 
 
@@ -860,15 +893,17 @@ def lin_dgrad(d: LinDesc, w: torch.Tensor, gz: torch.Tensor, gx: torch.Tensor | 
     """gx [P][Cin][N] = w^T·gz over the channels (see mqv_lin_dgrad), of
     gx_dtype (bfloat16 if not given)."""
     need = lin_workspace_bytes(d, OP_DGRAD)
-    dev = gz.device
-    wtp = _operand(w, "w", d.Cout * d.Cin, dev, torch.bfloat16)
-    gp = _operand(gz, "gz", d.P * d.Cout * d.N, dev, torch.bfloat16)
-    with _OnDevice(dev, stream) as on:
-        if gx is not None and gx_dtype is None:
-            gx_dtype = gx.dtype
-        gx, gxp = _result(gx, "gx", (d.P, d.Cin, d.N), gx_dtype or torch.bfloat16, dev)
-        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
-        _check(lib().mqv_lin_dgrad(ctypes.byref(d), wtp, gp, gxp, _TYPES[gx.dtype], wp, wn, on.handle))
+    P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    dev, at = _device_of(gz, "gz"), gz.device
+    wtp = _operand(w, "w", Cout * Cin, dev, _BF16)
+    gp = _operand(gz, "gz", P * Cout * N, dev, _BF16)
+    with _on(dev, stream):
+        if gx_dtype is None:
+            gx_dtype = _BF16 if gx is None else gx.dtype
+        gx = _result(gx, "gx", (P, Cin, N), P * Cin * N, gx_dtype, at)
+        ws, wp, wn = _layer_ws(ws, need, at)
+        _check(lib().mqv_lin_dgrad(ctypes.byref(d), wtp, gp, gx.data_ptr(), _TYPES[gx.dtype], wp, wn,
+                                   _raw_stream(dev)))
     return gx
 
 
@@ -876,11 +911,12 @@ def lin_wgrad(d: LinDesc, gz: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | 
               ws: torch.Tensor | None = None, stream=None):
     """gw [Cout][Cin] fp32 = sum over the columns of gz·x^T (see mqv_lin_wgrad)."""
     need = lin_workspace_bytes(d, OP_WGRAD)
-    dev = x.device
-    gp = _operand(gz, "gz", d.P * d.Cout * d.N, dev, torch.bfloat16)
-    xp = _operand(x, "x", d.P * d.Cin * d.N, dev, torch.bfloat16)
-    with _OnDevice(dev, stream) as on:
-        gw, gwp = _result(gw, "gw", (d.Cout, d.Cin), torch.float32, dev)
-        ws, wp, wn = _layer_ws(ws, need, dev) if need else (None, None, 0)
-        _check(lib().mqv_lin_wgrad(ctypes.byref(d), gp, xp, gwp, wp, wn, on.handle))
+    P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    dev, at = _device_of(x, "x"), x.device
+    gp = _operand(gz, "gz", P * Cout * N, dev, _BF16)
+    xp = _operand(x, "x", P * Cin * N, dev, _BF16)
+    with _on(dev, stream):
+        gw = _result(gw, "gw", (Cout, Cin), Cout * Cin, _F32, at)
+        ws, wp, wn = _layer_ws(ws, need, at)
+        _check(lib().mqv_lin_wgrad(ctypes.byref(d), gp, xp, gw.data_ptr(), wp, wn, _raw_stream(dev)))
     return gw
