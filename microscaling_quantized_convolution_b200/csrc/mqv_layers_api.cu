@@ -111,6 +111,7 @@ void launch_column_sum(const float* part, int64_t rows, int64_t n, int pairs, fl
 struct LnPlan {
   int v, k, group, groups;     // v: vector width; rows of scalars (v = 1) hold 2·k
   int tn, tiles, lanes, rows;
+  bool exact;                  // every thread has all its items
   int64_t units, blocks;
   int threads() const { return group * groups; }
 };
@@ -135,6 +136,7 @@ mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
     const int e = d->C <= 256 ? 8 : 16;
     pl->k = pl->v == 8 ? e / 8 : e / 2;
     pl->group = (int)(ceil_div(ceil_div(d->C, e), 32) * 32);
+    pl->exact = pl->v == 8 && d->C == (int64_t)pl->group * e;
     pl->units = d->P;
   } else {
     // K items of 4 (or 1) batch items a thread; the widest tile (up to 64
@@ -154,6 +156,7 @@ mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
           pl->tiles = (int)ceil_div(d->N, tn);
           pl->lanes = (int)lanes;
           pl->rows = (int)std::min<int64_t>(group / lanes, d->C);
+          pl->exact = v == 4 && d->N % tn == 0 && lanes * pl->rows == group && (int64_t)pl->rows * k == d->C;
           break;
         }
         if (tn <= v) break;
@@ -188,41 +191,44 @@ int64_t slot_bytes(const TensorIn& t, const LnPlan& pl, int depth) {
   return pl.v == 8 ? (int64_t)depth * pl.k * pl.threads() * (t.bf16 ? 16 : 32) : 0;
 }
 
-template <bool VEC, int K, int T, int B, bool KEEP>
+template <bool VEC, int K, int T, int B, bool KEEP, bool EXACT = false>
 cudaError_t launch_ln_fwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
-  return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP>, a, pl, slot_bytes(a.x, pl, 3), done, st);
+  return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP, EXACT>, a, pl, slot_bytes(a.x, pl, 3), done, st);
 }
 
 // The partial row is put together where the slots (or tiles' sums) were.
-template <bool VEC, int K, int T, int B, int D>
+template <bool VEC, int K, int T, int B, int D, bool EXACT = false>
 cudaError_t launch_ln_bwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
-  return launch_ln_kernel(ln_bwd_row_kernel<VEC, K, T, B, D>, a, pl,
+  return launch_ln_kernel(ln_bwd_row_kernel<VEC, K, T, B, D, EXACT>, a, pl,
                           std::max(slot_bytes(a.x, pl, D) + slot_bytes(a.gy, pl, D), 2 * (int64_t)a.C * 4), done, st);
 }
 
-template <int V, int K, int T>
+template <int V, int K, int T, bool EXACT = false>
 cudaError_t launch_ln_fwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, V);
-  return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T>, a, pl, sums, done, st);
+  return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T, EXACT>, a, pl, sums, done, st);
 }
 
-template <int V, int K, int T, int B>
+template <int V, int K, int T, int B, bool EXACT = false>
 cudaError_t launch_ln_bwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, 2 * V);
-  return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, st);
+  return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B, EXACT>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, st);
 }
 
+// Instances: EXACT ones for the usual widths, the others for the rest.
 cudaError_t launch_ln_fwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
   const int t = pl.threads();
   if (rows && pl.v == 8) {
     if (pl.k == 1) return launch_ln_fwd_rows<true, 1, 128, 6, true>(a, pl, st);
-    return t <= 256   ? launch_ln_fwd_rows<true, 2, 256, 3, true>(a, pl, st)
-           : t <= 512 ? launch_ln_fwd_rows<true, 2, 512, 1, true>(a, pl, st)
-                      : launch_ln_fwd_rows<true, 2, 1024, 1, false>(a, pl, st);
+    if (t <= 256)
+      return pl.exact ? launch_ln_fwd_rows<true, 2, 256, 3, true, true>(a, pl, st)
+                      : launch_ln_fwd_rows<true, 2, 256, 3, true>(a, pl, st);
+    return t <= 512 ? launch_ln_fwd_rows<true, 2, 512, 1, true>(a, pl, st)
+                    : launch_ln_fwd_rows<true, 2, 1024, 1, false>(a, pl, st);
   }
   if (rows) {
     if (pl.k == 4) return launch_ln_fwd_rows<false, 4, 128, 6, true>(a, pl, st);
@@ -230,7 +236,10 @@ cudaError_t launch_ln_fwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStre
            : t <= 512 ? launch_ln_fwd_rows<false, 8, 512, 1, true>(a, pl, st)
                       : launch_ln_fwd_rows<false, 8, 1024, 1, false>(a, pl, st);
   }
-  if (pl.v == 4) return t <= 512 ? launch_ln_fwd_tiles<4, 8, 512>(a, pl, st) : launch_ln_fwd_tiles<4, 8, 1024>(a, pl, st);
+  if (pl.v == 4) {
+    if (t > 512) return launch_ln_fwd_tiles<4, 8, 1024>(a, pl, st);
+    return pl.exact ? launch_ln_fwd_tiles<4, 8, 512, true>(a, pl, st) : launch_ln_fwd_tiles<4, 8, 512>(a, pl, st);
+  }
   return t <= 512 ? launch_ln_fwd_tiles<1, 16, 512>(a, pl, st) : launch_ln_fwd_tiles<1, 16, 1024>(a, pl, st);
 }
 
@@ -238,9 +247,11 @@ cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStre
   const int t = pl.threads();
   if (rows && pl.v == 8) {
     if (pl.k == 1) return launch_ln_bwd_rows<true, 1, 256, 2, 3>(a, pl, st);
-    return t <= 256   ? launch_ln_bwd_rows<true, 2, 256, 2, 3>(a, pl, st)
-           : t <= 512 ? launch_ln_bwd_rows<true, 2, 512, 1, 3>(a, pl, st)
-                      : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, st);
+    if (t <= 256)
+      return pl.exact ? launch_ln_bwd_rows<true, 2, 256, 2, 3, true>(a, pl, st)
+                      : launch_ln_bwd_rows<true, 2, 256, 2, 3>(a, pl, st);
+    return t <= 512 ? launch_ln_bwd_rows<true, 2, 512, 1, 3>(a, pl, st)
+                    : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, st);
   }
   if (rows) {
     if (pl.k == 4) return launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, st);
@@ -248,10 +259,11 @@ cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStre
            : t <= 512 ? launch_ln_bwd_rows<false, 8, 512, 1, 1>(a, pl, st)
                       : launch_ln_bwd_rows<false, 8, 1024, 1, 1>(a, pl, st);
   }
-  if (pl.v == 4)
-    return t <= 256   ? launch_ln_bwd_tiles<4, 8, 256, 2>(a, pl, st)
-           : t <= 512 ? launch_ln_bwd_tiles<4, 8, 512, 1>(a, pl, st)
-                      : launch_ln_bwd_tiles<4, 8, 1024, 1>(a, pl, st);
+  if (pl.v == 4) {
+    if (t > 512) return launch_ln_bwd_tiles<4, 8, 1024, 1>(a, pl, st);
+    if (t > 256) return launch_ln_bwd_tiles<4, 8, 512, 1>(a, pl, st);
+    return pl.exact ? launch_ln_bwd_tiles<4, 8, 256, 2, true>(a, pl, st) : launch_ln_bwd_tiles<4, 8, 256, 2>(a, pl, st);
+  }
   return t <= 512 ? launch_ln_bwd_tiles<1, 16, 512, 1>(a, pl, st) : launch_ln_bwd_tiles<1, 16, 1024, 1>(a, pl, st);
 }
 
@@ -433,7 +445,7 @@ void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
       if (s > fill) continue;
       const double wave = std::max(ceil_div(kblocks, s) * t.block, t.epilogue);
       double us = t.base + ceil_div(tiles * s, units) * wave;
-      if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.5e6;
+      if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.0e6;
       if (best == 0 || us < best) {
         best = us;
         pl->bn = t.bn;

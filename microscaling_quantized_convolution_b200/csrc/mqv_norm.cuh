@@ -292,8 +292,9 @@ __device__ __forceinline__ void slot_wait_all() { asm volatile("cp.async.wait_al
 
 // D: rows in flight; B: blocks an SM that the registers must allow; KEEP:
 // gamma and beta stay in registers, where there are some left, else they are
-// read again for each row (from L1).
-template <bool VEC, int K, int T, int B, int D, bool KEEP>
+// read again for each row (from L1); EXACT: every thread has all K vectors,
+// and nothing is tested.
+template <bool VEC, int K, int T, int B, int D, bool KEEP, bool EXACT>
 __global__ void __launch_bounds__(T, B) ln_fwd_row_kernel(const LnArgs a) {
   constexpr int V = VEC ? 8 : 2, kItems = VEC ? K : 2 * K;
   extern __shared__ __align__(16) uint8_t slots[];
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(T, B) ln_fwd_row_kernel(const LnArgs a) {
   const int groups = blockDim.x / grp.size;
   const int C = a.C, step = grp.size * (VEC ? V : 1), c0 = grp.tid * (VEC ? V : 1);
   const float inv = 1.f / C;
-  const uint32_t mask = items_below(c0, step, kItems, C);
+  const uint32_t mask = EXACT ? ~0u : items_below(c0, step, kItems, C);
   const uint32_t s0 = smem_u32(slots), slot_bytes = K * blockDim.x * (a.x.bf16 ? 16 : 32);
   const int first = blockIdx.x * groups + grp.index, hop = gridDim.x * groups;
   auto fetch = [&](int p, uint32_t slot) {
@@ -396,7 +397,7 @@ __device__ __forceinline__ void write_partial(const LnArgs& a, const G& grp, int
   for (int i = threadIdx.x; i < 2 * a.C; i += blockDim.x) part[i] = acc[i];
 }
 
-template <bool VEC, int K, int T, int B, int D>
+template <bool VEC, int K, int T, int B, int D, bool EXACT>
 __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
   constexpr int V = VEC ? 8 : 2, kItems = VEC ? K : 2 * K;
   extern __shared__ __align__(16) uint8_t slots[];
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
   const int groups = blockDim.x / grp.size;
   const int C = a.C, step = grp.size * (VEC ? V : 1), c0 = grp.tid * (VEC ? V : 1);
   const float inv = 1.f / C;
-  const uint32_t mask = items_below(c0, step, kItems, C);
+  const uint32_t mask = EXACT ? ~0u : items_below(c0, step, kItems, C);
   const uint32_t s0 = smem_u32(slots), x_bytes = K * blockDim.x * (a.x.bf16 ? 16 : 32);
   const uint32_t slot_bytes = x_bytes + K * blockDim.x * (a.gy.bf16 ? 16 : 32);
   const int first = blockIdx.x * groups + grp.index, hop = gridDim.x * groups;
@@ -623,7 +624,8 @@ __device__ __forceinline__ void store_items(const TensorOut& t, int64_t i, int64
   }
 }
 
-template <int V, int K, int T>
+// EXACT: every thread has all K items of every tile.
+template <int V, int K, int T, bool EXACT>
 __global__ void __launch_bounds__(T) ln_fwd_tile_kernel(const LnArgs a) {
   constexpr int H = (V + 1) / 2;
   extern __shared__ __align__(16) float sums[];
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(T) ln_fwd_tile_kernel(const LnArgs a) {
   const int64_t n = static_cast<int64_t>(u - p * a.tiles) * a.tn + l * V;
   const int sum_floats = tile_sum_floats(a.lanes, grp.size, V);
   float* buf = sums + grp.index * 2 * sum_floats;
-  const uint32_t mask = r < a.rows && l * V < a.tn && n < a.N ? items_below(r, a.rows, K, C) : 0;
+  const uint32_t mask = EXACT ? ~0u : r < a.rows && l * V < a.tn && n < a.N ? items_below(r, a.rows, K, C) : 0;
   const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n, step = a.rows * a.N;
   pair_t v[K][H], t[H];
   load_items<V, K>(a.x, at, step, mask, v);
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(T) ln_fwd_tile_kernel(const LnArgs a) {
   store_items<V, K>(a.out, at, step, mask, v);
 }
 
-template <int V, int K, int T, int B>
+template <int V, int K, int T, int B, bool EXACT>
 __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
   constexpr int H = (V + 1) / 2;
   extern __shared__ __align__(16) float sums[];
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
   const int64_t step = a.rows * a.N;
   const int sum_floats = tile_sum_floats(a.lanes, grp.size, 2 * V);
   float* buf = sums + grp.index * 2 * sum_floats;  // two, used in turn
-  const uint32_t items = r < a.rows && l * V < a.tn ? items_below(r, a.rows, K, C) : 0;
+  const uint32_t items = EXACT ? ~0u : r < a.rows && l * V < a.tn ? items_below(r, a.rows, K, C) : 0;
   float w[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) w[k] = a.gamma && (items >> k & 1) ? __ldg(a.gamma + r + k * a.rows) : 1.f;
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
   for (int u = blockIdx.x * groups + grp.index; u < a.units; u += gridDim.x * groups, turn ^= 1) {
     const int p = fdiv(u, a.by_tiles);
     const int64_t n = static_cast<int64_t>(u - p * a.tiles) * a.tn + l * V;
-    const uint32_t mask = n < a.N ? items : 0;
+    const uint32_t mask = EXACT || n < a.N ? items : 0;
     const int64_t at = (static_cast<int64_t>(p) * C + r) * a.N + n;
     pair_t x[K][H], g[K][H], mp[H], qp[H], t1[H], t2[H];
     load_items<V, K>(a.x, at, step, mask, x);
