@@ -85,19 +85,14 @@ __device__ __forceinline__ void group_sum(const G& g, float (&v)[M], float* buf)
 
 // ------------------------------------------------------- vectors as pairs
 
-// V fp32 elements (8, 4 or 2 scalars `apart` elements from each other) as
-// V / 2 pairs; p is their first element.
-template <bool VEC, int V>
-__device__ __forceinline__ void load_pairs(const float* p, int64_t apart, bool second, pair_t (&v)[V / 2]) {
-  if constexpr (!VEC) {
-    v[0] = pair(__ldg(p), second ? __ldg(p + apart) : 0.f);
-  } else {
+// V fp32 elements from p as pairs.
+template <int H>
+__device__ __forceinline__ void load_vector(const float* p, pair_t (&v)[H]) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[2 * i] = pair(t.x, t.y);
-      v[2 * i + 1] = pair(t.z, t.w);
-    }
+  for (int i = 0; i < H / 2; ++i) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(p) + i);
+    v[2 * i] = pair(t.x, t.y);
+    v[2 * i + 1] = pair(t.z, t.w);
   }
 }
 
@@ -422,9 +417,15 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) fetch(first + i * hop, s0 + i * slot_bytes);
-  // ag, ab: sums of gy·xh and gy; gamma comes in again for each row (from L1),
-  // which costs fewer registers than it saves
-  pair_t ag[K][V / 2], ab[K][V / 2];
+  // ag, ab: sums of gy·xh and gy.  Vectors of gamma come in again for each row
+  // (from L1), which leaves the registers to more warps; scalars would wait for
+  // one another, and are kept
+  pair_t ag[K][V / 2], ab[K][V / 2], gam[VEC ? 1 : K][V / 2];
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) gam[k][0] = pair(1.f, 1.f);
+    if (a.gamma) load_all<VEC, V, K>(TensorIn{a.gamma, 0}, c0, step, mask, gam);
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -458,12 +459,15 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
         ag[k][i] = fma2(g[k][i], x[k][i], ag[k][i]);
         ab[k][i] = add2(ab[k][i], g[k][i]);
       }
-    if (a.gamma) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) g[k][0] = mul2(g[k][0], gam[k][0]);
+    } else if (a.gamma) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (mask >> (VEC ? k : 2 * k) & 1) {
+        if (mask >> k & 1) {
           pair_t w[V / 2];
-          load_pairs<VEC, V>(a.gamma + c0 + (VEC ? k : 2 * k) * step, step, mask >> (2 * k + 1) & 1, w);
+          load_vector(a.gamma + c0 + k * step, w);
 #pragma unroll
           for (int i = 0; i < V / 2; ++i) g[k][i] = mul2(g[k][i], w[i]);
         }
@@ -703,9 +707,9 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
   float w[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) w[k] = a.gamma && (items >> k & 1) ? __ldg(a.gamma + r + k * a.rows) : 1.f;
-  pair_t ag[K], ab[K];
+  float ag[K], ab[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) ag[k] = ab[k] = 0;
+  for (int k = 0; k < K; ++k) ag[k] = ab[k] = 0.f;
   int turn = 0;
   for (int u = blockIdx.x * groups + grp.index; u < a.units; u += gridDim.x * groups, turn ^= 1) {
     const int p = fdiv(u, a.by_tiles);
@@ -730,16 +734,21 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
 #pragma unroll
     for (int i = 0; i < H; ++i) t1[i] = t2[i] = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      const pair_t wk = pair(w[k], w[k]);
+      pair_t tg = 0, tb = 0;
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         x[k][i] = mul2(add2(x[k][i], mp[i]), qp[i]);       // outside: gy is 0
-        ag[k] = fma2(g[k][i], x[k][i], ag[k]);
-        ab[k] = add2(ab[k], g[k][i]);
-        g[k][i] = mul2(g[k][i], pair(w[k], w[k]));
+        tg = fma2(g[k][i], x[k][i], tg);
+        tb = add2(tb, g[k][i]);
+        g[k][i] = mul2(g[k][i], wk);
         t1[i] = add2(t1[i], g[k][i]);
         t2[i] = fma2(g[k][i], x[k][i], t2[i]);
       }
+      ag[k] += lo(tg) + hi(tg);
+      ab[k] += lo(tb) + hi(tb);
+    }
     float s[2 * V], s1[V], s2[V];
     spread<V>(t1, s1);
     spread<V>(t2, s2);
@@ -759,19 +768,13 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
   pdl_launch_dependents();
   if (!a.part) return;
   // a channel's sums over the lanes of its row, then over the groups
-  float fg[K], fb[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    fg[k] = lo(ag[k]) + hi(ag[k]);
-    fb[k] = lo(ab[k]) + hi(ab[k]);
-  }
   int turns = a.lanes;
   if (tile_sum_by_warps(a.lanes)) {
     for (int o = a.lanes >> 1; o > 0; o >>= 1)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        fg[k] += __shfl_xor_sync(0xffffffffu, fg[k], o);
-        fb[k] += __shfl_xor_sync(0xffffffffu, fb[k], o);
+        ag[k] += __shfl_xor_sync(0xffffffffu, ag[k], o);
+        ab[k] += __shfl_xor_sync(0xffffffffu, ab[k], o);
       }
     turns = 1;
   }
@@ -780,8 +783,8 @@ __global__ void __launch_bounds__(T, B) ln_bwd_tile_kernel(const LnArgs a) {
     for (int k = 0; k < K; ++k) {
       const int c = r + k * a.rows;
       if (r < a.rows && c < C) {
-        acc[c] += fg[k];
-        acc[C + c] += fb[k];
+        acc[c] += ag[k];
+        acc[C + c] += ab[k];
       }
     }
   });
