@@ -68,6 +68,7 @@ struct GemmTcArgs {
   GemmOperand a, b;
   int tiles_m, tiles_n, splits, kblocks;
   int tail_width;              // N tiles of the last band (see gemm_tile)
+  int run;                     // K blocks summed by one accumulator (see gemm_add_runs)
   FastDiv by_split, by_band, by_tail, by_pos;   // divisions by tiles of a split, of a band, tail_width, col_per_pos
   // output element (row, column c of chunk q = c / col_chunk):
   //   (q / col_per_pos)·pos + row·row_stride + (q % col_per_pos)·col_chunk + c % col_chunk
@@ -490,6 +491,49 @@ __device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const Ge
   return true;
 }
 
+// The tensor cores' running sum loses more than a rounding at each step: over
+// 1400 products it is off by 1.4e-6 (2-norm, of operands whose channels have
+// offsets), and more the longer it runs.  Results that are kept in fp32 are
+// therefore summed in runs of g.run K blocks; the epilogue warps add the runs'
+// sums in registers, rounding to nearest, and put the total in the place of
+// the last run's accumulator.  The tensor cores go on meanwhile with the other
+// accumulator.  `tmem`: the first accumulator at the warp's lanes and columns;
+// `nt` counts the CTA's runs.  False if a wait gave up.
+template <int BN, int COLS, typename F>
+__device__ __forceinline__ bool gemm_add_runs(const GemmTcArgs& g, uint32_t tmem, int runs, uint32_t& nt,
+                                              uint64_t* acc_full, F release) {
+  float sum[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) sum[i] = 0.f;
+  for (int run = 0; run < runs; ++run) {
+    const int buf = nt & 1;
+    if (!mbar_wait_bounded(acc_full + buf, (nt / 2) & 1, g.err, 4)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < COLS; k += 32) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem + buf * BN + k, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[k + i] += __uint_as_float(r[i]);
+    }
+    if (run + 1 < runs) {
+      tc_fence_before();
+      release(buf);
+      ++nt;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < COLS; k += 32) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[k + i]);
+    tmem_st_32x32b_x32(tmem + (nt & 1) * BN + k, r);
+  }
+  tmem_st_wait();
+  return true;
+}
+
 // The same without TMA: half of the tile's columns from col0, 16 at a time
 // through the warp's staging rows `st`.
 template <int COLS, typename F>
@@ -541,7 +585,8 @@ template <int BN, bool PAIR, bool FAST>
 constexpr int gemm_smem = 1024 + gemm_stages<BN, PAIR> * gemm_stage_bytes<BN, PAIR> +
                           kGemmEpiWarps * kGemmEpiWarpBytes<FAST> + 1536;
 
-template <int BN, bool PAIR, bool FAST>
+// RUNS: the sums may go in several runs of K blocks.
+template <int BN, bool PAIR, bool FAST, bool RUNS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmTcArgs g) {
   constexpr int kStages = gemm_stages<BN, PAIR>, kStageBytes = gemm_stage_bytes<BN, PAIR>;
@@ -641,16 +686,20 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     uint32_t nt = 0, round = 0;
     int s = 0;
     bool live = true;
-    for (int t = first; t < tiles && live; t += step, ++nt) {
+    for (int t = first; t < tiles && live; t += step) {
       const GemmTile tl = gemm_tile(g, t);
       const int kn = share + (tl.split < extra);
-      const int buf = nt & 1;
-      if (nt >= 2 && !warp_wait(acc_empty + buf, (nt / 2 - 1) & 1, g.err, 4)) {
-        live = false;
-        break;
-      }
-      tc_fence_after();
+      int left = 0;                                // K blocks of this run still to come
       for (int k = 0; k < kn; ++k) {
+        const int buf = nt & 1;
+        const bool begin = left == 0;
+        if (begin) {
+          left = RUNS ? min(g.run, kn - k) : kn;
+          if (nt >= 2 && !warp_wait(acc_empty + buf, (nt / 2 - 1) & 1, g.err, 4)) {
+            live = false;
+            break;
+          }
+        }
         if (!warp_wait(full + s, round & 1, g.err, 2)) {
           live = false;
           break;
@@ -661,17 +710,17 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             gemm_mma<PAIR>(tmem + buf * BN, da | (base + sa[q]), db | (base + (kABytes >> 4) + sb[q]), idesc,
-                           k > 0 || q > 0);
+                           !begin || q > 0);
           gemm_commit<PAIR>(empty + s);
+          if (left == 1) gemm_commit<PAIR>(acc_full + buf);
         }
         __syncwarp();
+        if (--left == 0) ++nt;
         if (++s == kStages) {
           s = 0;
           ++round;
         }
       }
-      if (elect_one()) gemm_commit<PAIR>(acc_full + buf);
-      __syncwarp();
     }
   } else if (warp >= 2) {
     // ---- epilogue: warp w reads tensor-memory lanes 32·(w % 4).., half of the columns
@@ -680,20 +729,26 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     uint32_t nt = 0, used = 0;
     for (int t = first; t < tiles; t += step, ++nt) {
       const GemmTile tl = gemm_tile(g, t);
-      const int buf = nt & 1;
       const int row0 = (tl.m * kCtas + rank) * kGemmBM + quad * 32;
       const int c0 = half * (BN / 2);
-      const uint32_t acc = tmem + buf * BN + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-      // the accumulator is read: the MMA warp may overwrite it
-      auto release = [&] {
+      const uint32_t acc0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
+      // an accumulator is read: the MMA warp may overwrite it
+      auto release_buf = [&](int b) {
         __syncwarp();
         if (lane == 0) {
           if constexpr (PAIR)
-            mbar_arrive_cluster(cluster_addr(acc_empty + buf, 0));
+            mbar_arrive_cluster(cluster_addr(acc_empty + b, 0));
           else
-            mbar_arrive(acc_empty + buf);
+            mbar_arrive(acc_empty + b);
         }
       };
+      if constexpr (RUNS) {
+        const int kn = share + (tl.split < extra);
+        if (kn > g.run && !gemm_add_runs<BN, BN / 2>(g, acc0, (kn + g.run - 1) / g.run, nt, acc_full, release_buf)) break;
+      }
+      const int buf = nt & 1;
+      const uint32_t acc = acc0 + buf * BN;
+      auto release = [&] { release_buf(buf); };
       if constexpr (FAST) {
         const bool bf = !g.part && g.e.d.bf16;
         if (!(bf ? gemm_epilogue_fast<BN / 2, true>(g, maps, acc, smem_u32(st), row0, tl.n * BN + c0, tl.split, used,

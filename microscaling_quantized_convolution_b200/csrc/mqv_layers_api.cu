@@ -131,9 +131,10 @@ mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
   if (d->N == 1) {
     // 16 values per thread, which with their parameters (and backward the
     // parameters' gradients) is what registers hold at 512 to 768 threads an
-    // SM; 8 for short rows
+    // SM; 8 for short rows, and for scalars backward, which are not prefetched
+    // (4097 x 1023: 20 us against 21)
     pl->v = d->C % 8 == 0 ? 8 : 1;
-    const int e = d->C <= 256 ? 8 : 16;
+    const int e = d->C <= 256 || (bwd && pl->v == 1 && d->C <= 4096) ? 8 : 16;
     pl->k = pl->v == 8 ? e / 8 : e / 2;
     pl->group = (int)(ceil_div(ceil_div(d->C, e), 32) * 32);
     pl->exact = pl->v == 8 && d->C == (int64_t)pl->group * e;
@@ -575,10 +576,10 @@ mqv_status encode_output(CUtensorMap* map, const void* p, bool f32, const GemmTc
   return encode(map, f32, 4, p, dims, strides, box);
 }
 
-template <int BN, bool PAIR, bool FAST>
+template <int BN, bool PAIR, bool FAST, bool RUNS>
 cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
   static bool done[kMaxDevices] = {};
-  auto kernel = gemm_tc_kernel<BN, PAIR, FAST>;
+  auto kernel = gemm_tc_kernel<BN, PAIR, FAST, RUNS>;
   const cudaError_t e = allow_smem(kernel, gemm_smem<BN, PAIR, FAST>, done);
   if (e != cudaSuccess) return e;
   constexpr int kCtas = PAIR ? 2 : 1;
@@ -597,10 +598,11 @@ cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, maps, pl.args);
 }
 
-template <bool FAST>
+template <bool FAST, bool RUNS>
 cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
-  if (pl.pair) return launch_gemm_tile<256, true, FAST>(pl, maps, st);
-  return pl.bn == 128 ? launch_gemm_tile<128, false, FAST>(pl, maps, st) : launch_gemm_tile<64, false, FAST>(pl, maps, st);
+  if (pl.pair) return launch_gemm_tile<256, true, FAST, RUNS>(pl, maps, st);
+  return pl.bn == 128 ? launch_gemm_tile<128, false, FAST, RUNS>(pl, maps, st)
+                      : launch_gemm_tile<64, false, FAST, RUNS>(pl, maps, st);
 }
 
 // Copies an operand whose rows are unaligned; *p then points at the copy.
@@ -631,6 +633,8 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
   g.e = e;
   g.e.vec4 = plan_e.vec4;
   g.e.bias_on_row = plan_e.bias_on_row;
+  // results kept in fp32: runs of 512 products, else one run
+  g.run = g.e.d.bf16 ? g.kblocks : 8;
   char* w = static_cast<char*>(ws);
   if (g.splits > 1) g.part = reinterpret_cast<float*>(w);
   w += pl.part_bytes;
@@ -649,7 +653,9 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
     if (!g.part && g.e.z.p && (s = encode_output(&maps.z, g.e.z.p, false, g))) return s;
     if (!g.part && g.e.residual && (s = encode_output(&maps.residual, g.e.residual, !g.e.d.bf16, g))) return s;
   }
-  const cudaError_t ce = fast ? launch_gemm<true>(pl, maps, st) : launch_gemm<false>(pl, maps, st);
+  const bool runs = ceil_div(g.kblocks, g.splits) > g.run;
+  const cudaError_t ce = fast ? (runs ? launch_gemm<true, true>(pl, maps, st) : launch_gemm<true, false>(pl, maps, st))
+                              : (runs ? launch_gemm<false, true>(pl, maps, st) : launch_gemm<false, false>(pl, maps, st));
   if (ce != cudaSuccess) return cuda_fail(ce, "linear layer launch");
   if (g.splits > 1) {
     const int64_t inner = g.e.bias_on_row ? g.col_inner : 1, channels = g.e.bias_on_row ? pl.M : g.col_inner;

@@ -21,6 +21,8 @@ LIN_PIXELS = [(1, 3, 5, 2), (7, 16, 8, 4), (49, 64, 64, 16), (5, 33, 40, 12), (4
 # enough tiles for two-CTA tiles of 256 x 256 or 256 x 128 in one pass or another
 LIN_WIDE = [(2500, 40, 1992, 1), (2300, 72, 2047, 1), (1300, 64, 1608, 1), (65, 1992, 2500, 1), (600, 264, 280, 16),
             (300, 264, 520, 32), (150, 260, 264, 64), (150, 264, 296, 80)]
+# contractions longer than one accumulator's run, K not split to shorter ones
+LIN_LONG = [(1280, 1100, 1000, 1), (1270, 1100, 1003, 1), (90, 1000, 1100, 8)]
 
 
 def shape_id(s):

@@ -7,7 +7,7 @@ import torch
 
 import microscaling_quantized_convolution_b200 as mqv
 from oracle import layers_oracle as L
-from tests.layers_cases import LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES, activations, shape_id, stored
+from tests.layers_cases import LIN_LONG, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES, activations, shape_id, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -148,7 +148,7 @@ def lin_inputs(shape, seed=0):
             rng.standard_normal((P, Cout, N)), rng.standard_normal((P, Cout, N)) * 1e-2)
 
 
-@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE, ids=shape_id)
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG, ids=shape_id)
 def test_linear_layer(shape):
     P, Cin, Cout, N = shape
     w, x, bias, res, gy = lin_inputs(shape)

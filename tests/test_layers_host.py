@@ -10,7 +10,7 @@ import torch
 import microscaling_quantized_convolution_b200 as mqv
 from microscaling_quantized_convolution_b200 import build as mqv_build
 from oracle import layers_oracle as L
-from tests.layers_cases import LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES
+from tests.layers_cases import LIN_LONG, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -94,7 +94,7 @@ def test_ln_accepts_every_test_shape(shape):
     assert b % 256 == 0 and (b > 0 or shape[0] == 0)
 
 
-@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + [(0, 5, 6, 1), (0, 64, 32, 16)])
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG + [(0, 5, 6, 1), (0, 64, 32, 16)])
 def test_lin_accepts_every_test_shape(shape):
     d = mqv.lin_desc(*shape)
     for op in (mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD, mqv.OP_ACT_GRAD):
