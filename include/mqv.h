@@ -398,7 +398,8 @@ mqv_status mqv_dw_wgrad(const mqv_dw_desc* d, const void* gy, const void* x, flo
  * run to run.
  * Validation, common to all of them: C (Cin, Cout) and N positive, P >= 0
  * (P = 0: nothing is read, gradients of parameters are written as zeros),
- * fewer than 2^31 columns, every buffer 16-byte aligned device memory the
+ * fewer than 2^31 - 2^16 columns (for the linear layer with N rounded up to
+ * 64) and 2^37 elements a tensor, every buffer 16-byte aligned device memory the
  * caller owns; no written buffer may overlap another buffer of the call
  * unless stated.  Failures return before anything is launched.  Calls that
  * overlap on the GPU need workspaces of their own. */
@@ -472,7 +473,7 @@ mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, f
                          void* stream);
 
 /* Synchronizes `stream`, then reports and clears the device error word that
- * bounded waits inside the conv kernels set when they give up
+ * bounded waits inside the conv and linear-layer kernels set when they give up
  * (*flags = 0: none).  Returns MQV_ERR_TIMEOUT if a flag was set.  Bits:
  * 1 a wait for a free pipeline stage, 2 a wait for a filled stage, 4 a wait
  * for a finished accumulator, 8 the wait of mqv_selftest_wait_timeout.

@@ -8,6 +8,7 @@ missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -648,7 +649,8 @@ def dw_wgrad(d: DwDesc, gy: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | No
 
 _F32, _BF16 = torch.float32, torch.bfloat16
 _TYPES = {_F32: 0, _BF16: 1}
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current stream's handle; the public call builds a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 class _OnStream:
@@ -745,6 +747,19 @@ def ln_desc(P, C, N=1, eps=1e-5) -> LnDesc:
     return LnDesc(P, C, N, eps, 0)
 
 
+@functools.lru_cache(maxsize=1024)
+def _ln_ws(P, C, N, eps) -> int:
+    """ln_bwd's workspace bytes, asked for once per shape."""
+    return ln_bwd_workspace_bytes(LnDesc(P, C, N, eps, 0))
+
+
+@functools.lru_cache(maxsize=4096)
+def _lin_ws(P, Cin, Cout, N, act, op) -> int:
+    """A linear pass's workspace bytes, asked for once per shape; raises for a
+    bad descriptor, each time."""
+    return lin_workspace_bytes(LinDesc(P, Cin, Cout, N, act, 0), op)
+
+
 def ln_bwd_workspace_bytes(d: LnDesc) -> int:
     """Workspace bytes of ln_bwd; raises MqvError for an invalid descriptor."""
     b = ctypes.c_size_t()
@@ -807,7 +822,7 @@ def ln_bwd(d: LnDesc, gy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
             ggamma = _result(ggamma, "ggamma", (C,), C, _F32, at)
             gbeta = _result(gbeta, "gbeta", (C,), C, _F32, at)
             ggp, gbp = ggamma.data_ptr(), gbeta.data_ptr()
-            ws, wp, wn = _layer_ws(ws, ln_bwd_workspace_bytes(d), at)
+            ws, wp, wn = _layer_ws(ws, _ln_ws(P, C, N, d.eps), at)
         _check(lib().mqv_ln_bwd(ctypes.byref(d), gyp, _TYPES[gy.dtype], xp, _TYPES[x.dtype], mp, rp, gp, gx.data_ptr(),
                                 _TYPES[gx.dtype], ggp, gbp, wp, wn, _raw_stream(dev)))
     return gx, ggamma, gbeta
@@ -834,8 +849,8 @@ def lin_fwd(d: LinDesc, w: torch.Tensor, x: torch.Tensor, bias: torch.Tensor | N
     (see mqv_lin_fwd), of y_dtype (the residual's, else bfloat16, if not
     given); z, the bfloat16 pre-activation that lin_act_grad takes, with
     save_z=True (or into the z given), else None.  w: bfloat16 [Cout][Cin]."""
-    need = lin_workspace_bytes(d, OP_FWD)
     P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    need = _lin_ws(P, Cin, Cout, N, d.act, OP_FWD)
     dev, at = _device_of(x, "x"), x.device
     n = P * Cout * N
     wtp = _operand(w, "w", Cout * Cin, dev, _BF16)
@@ -860,8 +875,8 @@ def lin_act_grad(d: LinDesc, gy: torch.Tensor, z: torch.Tensor | None = None, gz
     """(gz, gbias): gz = gy·act'(z) in bfloat16 and its fp32 sum over the
     columns, gbias [Cout] (None with bias_grad=False; see mqv_lin_act_grad).
     With act "none", a bfloat16 gy and no gz given, gz is gy itself."""
-    need = lin_workspace_bytes(d, OP_ACT_GRAD)
     P, Cout, N = d.P, d.Cout, d.N
+    need = _lin_ws(P, d.Cin, Cout, N, d.act, OP_ACT_GRAD)
     dev, at = _device_of(gy, "gy"), gy.device
     n = P * Cout * N
     gyp = _operand(gy, "gy", n, dev)
@@ -892,8 +907,8 @@ def lin_dgrad(d: LinDesc, w: torch.Tensor, gz: torch.Tensor, gx: torch.Tensor | 
               ws: torch.Tensor | None = None, stream=None):
     """gx [P][Cin][N] = w^T·gz over the channels (see mqv_lin_dgrad), of
     gx_dtype (bfloat16 if not given)."""
-    need = lin_workspace_bytes(d, OP_DGRAD)
     P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    need = _lin_ws(P, Cin, Cout, N, d.act, OP_DGRAD)
     dev, at = _device_of(gz, "gz"), gz.device
     wtp = _operand(w, "w", Cout * Cin, dev, _BF16)
     gp = _operand(gz, "gz", P * Cout * N, dev, _BF16)
@@ -910,8 +925,8 @@ def lin_dgrad(d: LinDesc, w: torch.Tensor, gz: torch.Tensor, gx: torch.Tensor | 
 def lin_wgrad(d: LinDesc, gz: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | None = None,
               ws: torch.Tensor | None = None, stream=None):
     """gw [Cout][Cin] fp32 = sum over the columns of gz·x^T (see mqv_lin_wgrad)."""
-    need = lin_workspace_bytes(d, OP_WGRAD)
     P, Cin, Cout, N = d.P, d.Cin, d.Cout, d.N
+    need = _lin_ws(P, Cin, Cout, N, d.act, OP_WGRAD)
     dev, at = _device_of(x, "x"), x.device
     gp = _operand(gz, "gz", P * Cout * N, dev, _BF16)
     xp = _operand(x, "x", P * Cin * N, dev, _BF16)

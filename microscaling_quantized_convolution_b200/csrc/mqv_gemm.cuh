@@ -689,37 +689,35 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
     for (int t = first; t < tiles && live; t += step) {
       const GemmTile tl = gemm_tile(g, t);
       const int kn = share + (tl.split < extra);
-      int left = 0;                                // K blocks of this run still to come
-      for (int k = 0; k < kn; ++k) {
-        const int buf = nt & 1;
-        const bool begin = left == 0;
-        if (begin) {
-          left = RUNS ? min(g.run, kn - k) : kn;
-          if (nt >= 2 && !warp_wait(acc_empty + buf, (nt / 2 - 1) & 1, g.err, 4)) {
-            live = false;
-            break;
-          }
-        }
-        if (!warp_wait(full + s, round & 1, g.err, 2)) {
+      for (int k0 = 0; k0 < kn && live; k0 += RUNS ? g.run : kn, ++nt) {
+        const int buf = nt & 1, end = RUNS ? min(k0 + g.run, kn) : kn;
+        if (nt >= 2 && !warp_wait(acc_empty + buf, (nt / 2 - 1) & 1, g.err, 4)) {
           live = false;
           break;
         }
         tc_fence_after();
-        const uint32_t base = base0 + s * (kStageBytes >> 4);
-        if (elect_one()) {
+        for (int k = k0; k < end; ++k) {
+          if (!warp_wait(full + s, round & 1, g.err, 2)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t base = base0 + s * (kStageBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            gemm_mma<PAIR>(tmem + buf * BN, da | (base + sa[q]), db | (base + (kABytes >> 4) + sb[q]), idesc,
-                           !begin || q > 0);
-          gemm_commit<PAIR>(empty + s);
-          if (left == 1) gemm_commit<PAIR>(acc_full + buf);
+            for (int q = 0; q < 4; ++q)
+              gemm_mma<PAIR>(tmem + buf * BN, da | (base + sa[q]), db | (base + (kABytes >> 4) + sb[q]), idesc,
+                             k > k0 || q > 0);
+            gemm_commit<PAIR>(empty + s);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ++round;
+          }
         }
+        if (elect_one()) gemm_commit<PAIR>(acc_full + buf);
         __syncwarp();
-        if (--left == 0) ++nt;
-        if (++s == kStages) {
-          s = 0;
-          ++round;
-        }
       }
     }
   } else if (warp >= 2) {

@@ -20,7 +20,7 @@ using namespace mqv;
 
 constexpr int kSms = 148;
 constexpr int64_t kMaxChannels = 16384;             // layer norm: a position's channels in one block's registers
-constexpr int64_t kMaxElements = int64_t{1} << 38;
+constexpr int64_t kMaxElements = int64_t{1} << 37;            // TMA strides stay below 2^40 bytes
 constexpr int64_t kMaxColumns = (int64_t{1} << 31) - (1 << 16);   // with a tile's overhang still an int
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -423,20 +423,22 @@ GemmOperand operand_of(const GemmView& v, int rows, bool batch) {
 }
 
 // The tile and the split of K with the least time by a model of the measured
-// times (us): a launch of one wave of tiles takes `base` (launch, first loads,
-// last epilogue) and `block` a K block; a wave is no shorter than the epilogue
-// that it overlaps with.  Measured at 8192 tokens 4096 -> 4096: 166 us in
-// 256 x 256 tiles of two CTAs, 279 in 128 x 128, 527 in 128 x 64; at 128
-// tokens 1024 -> 1024: 14.3, 10.8 and 8.8; 256 x 128 tiles of two CTAs were
-// never faster than 128 x 128.  A split writes and reads fp32 partial sums
-// and takes a second kernel.
+// times (us): `base` for launch, first loads and last epilogue, and for each
+// wave of tiles `start` and `block` for each K block, or `epilogue` where that
+// takes longer.  Measured (and modelled) for 8192 tokens, us in 256 x 256 tiles
+// of two CTAs, 128 x 128 and 128 x 64: 64 -> 4096 33, 31, 32 (33, 33, 35); 256
+// -> 4096 36, 36, 57 (34, 36, 60); 1024 -> 4096 57, 90, 154 (57, 90, 156); for
+// 2048 tokens 64 -> 1024 9.2, 6.5, 6.3 (8.6, 6.5, 6.7).  256 x 128 tiles of two
+// CTAs were never faster than 128 x 128.  A split writes and reads fp32
+// partial sums and takes a second kernel.
 void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
   struct Tile {
     int bn;
     bool pair;
-    double base, block, epilogue;
+    double start, block, epilogue;
   };
-  static constexpr Tile kTiles[] = {{256, true, 9.2, .37, 4.6}, {128, false, 6.0, .31, 2.4}, {64, false, 4.5, .29, 1.2}};
+  static constexpr Tile kTiles[] = {{256, true, 1.7, .36, 4.1}, {128, false, .95, .32, 2.0}, {64, false, .85, .285, 1.1}};
+  constexpr double kBase = 4.5;
   double best = 0;
   for (const Tile& t : kTiles) {
     const int64_t units = t.pair ? kSms / 2 : kSms;
@@ -444,8 +446,8 @@ void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
     const int64_t fill = std::max<int64_t>(1, std::min(units / tiles, kblocks / 2));
     for (int64_t s : {int64_t{1}, int64_t{2}, int64_t{4}, int64_t{8}, int64_t{16}, int64_t{32}, fill}) {
       if (s > fill) continue;
-      const double wave = std::max(ceil_div(kblocks, s) * t.block, t.epilogue);
-      double us = t.base + ceil_div(tiles * s, units) * wave;
+      const double wave = std::max(t.start + ceil_div(kblocks, s) * t.block, t.epilogue);
+      double us = kBase + ceil_div(tiles * s, units) * wave;
       if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.0e6;
       if (best == 0 || us < best) {
         best = us;
