@@ -24,6 +24,15 @@
 // The backward groups run over many rows or tiles and keep their channels'
 // parameter gradients in registers; a block adds its groups' in order and
 // writes one partial row, and column_sum_kernel adds the rows in a fixed order.
+//
+// Measured, L2 flushed: forward 16384 x 4096 bfloat16 47 us (5.7 TB/s, 0.89 of
+// the copy rate), 80 x 80 pixels of 64 channels at batch 16, fp32 to bfloat16,
+// 8.6 us (0.72); backward 8192 x 4096 54 us (3.7 TB/s, 0.57: instruction issue
+// and latency at the 512 threads an SM that the registers allow), 56 x 56
+// pixels of 128 channels at batch 64 in fp32 61 us (0.79), 28 x 28 20 us (2.65
+// tiles a group: the last round is not full).  8 instead of 16 values a thread
+// at twice the threads are slower (64 us for 8192 x 4096 backward), so are 80
+// registers for a third block (76 us, spills), or a prefetch of tiles (no gain).
 #pragma once
 
 #include "mqv_layer_common.cuh"
