@@ -418,7 +418,8 @@ typedef struct {
  * (sum_c (x - mean)^2 / C + eps)^(-1/2) of each column.  gamma, beta: [C],
  * NULL for 1 and 0.  mean, rstd: [P][N], both NULL if not kept.  y may be x
  * itself when their types are the same.  A NaN or infinity in a column makes
- * that column NaN and no other. */
+ * that column NaN and no other.  With eps = 0 a constant column has no defined
+ * result (0 / 0, up to the mean's rounding) and leaves the others alone. */
 mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const float* gamma, const float* beta,
                       void* y, int32_t y_type, float* mean, float* rstd, void* stream);
 

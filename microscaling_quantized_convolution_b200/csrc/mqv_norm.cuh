@@ -41,7 +41,7 @@
 namespace mqv {
 
 struct LnArgs {
-  int64_t P, N;
+  int64_t N;
   int C;
   float eps;
   const float *gamma, *beta;   // null: 1 and 0

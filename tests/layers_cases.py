@@ -9,7 +9,8 @@ LN_ROWS = [(1, 1, 1), (1, 8, 1), (3, 7, 1), (1, 1024, 1), (5, 1023, 1), (2, 2048
 # Batch columns: one channel, odd batches, whole and ragged tiles of 64 batch
 # items, more channels than the widest tile takes, a large batch.
 LN_TILES = [(1, 1, 2), (3, 5, 3), (7, 64, 16), (4, 128, 64), (2, 512, 64), (2, 2048, 8), (1, 4096, 4), (1, 16384, 4),
-            (1, 5000, 3), (5, 33, 84), (2, 16, 200), (3, 20, 12), (1, 3, 10240), (600, 16, 4), (800, 24, 32)]
+            (1, 5000, 3), (5, 33, 84), (2, 16, 200), (3, 20, 12), (6, 64, 20), (2, 256, 20), (1, 3, 10240),
+            (600, 16, 4), (800, 24, 32)]
 
 # (P, Cin, Cout, N)
 LIN_TOKENS = [(1, 1, 1, 1), (1, 64, 64, 1), (1, 1000, 1003, 1), (2, 2048, 96, 1), (3, 5, 7, 1), (8, 1000, 1003, 1),
@@ -17,7 +18,8 @@ LIN_TOKENS = [(1, 1, 1, 1), (1, 64, 64, 1), (1, 1000, 1003, 1), (2, 2048, 96, 1)
               (513, 96, 200, 1), (300, 1024, 264, 1), (1, 4096, 512, 1), (1025, 128, 640, 1), (33, 520, 1024, 1)]
 LIN_PIXELS = [(1, 3, 5, 2), (7, 16, 8, 4), (49, 64, 64, 16), (5, 33, 40, 12), (4, 128, 256, 64), (3, 64, 100, 84),
               (10, 24, 24, 8), (3, 40, 48, 32), (2, 16, 16, 200), (6, 65, 63, 16), (1, 128, 128, 96), (30, 64, 128, 24),
-              (1, 200, 72, 7), (100, 16, 24, 16), (2, 136, 320, 128)]
+              (1, 200, 72, 7), (100, 16, 24, 16), (2, 136, 320, 128), (9, 48, 72, 20), (5, 64, 64, 40),
+              (1, 72, 64, 256)]
 # enough tiles for two-CTA tiles of 256 x 256 or 256 x 128 in one pass or another
 LIN_WIDE = [(2500, 40, 1992, 1), (2300, 72, 2047, 1), (1300, 64, 1608, 1), (65, 1992, 2500, 1), (600, 264, 280, 16),
             (300, 264, 520, 32), (150, 260, 264, 64), (150, 264, 296, 80)]
