@@ -250,7 +250,12 @@ __device__ __forceinline__ void act_grad_run(const ActGradArgs& a, int64_t at, i
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (i + r >= count) break;
-      if constexpr (ACT != kActNone) {
+      if constexpr (ACT == kActRelu) {
+        // selected, not multiplied: where the unit is off, a gradient that
+        // overflowed to infinity is dropped like any other
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[r][e] = z[r][e] > 0.f ? g[r][e] : 0.f;
+      } else if constexpr (ACT != kActNone) {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           const pair_t s = slope_pair<ACT>(pair(z[r][e], e + 1 < V ? z[r][e + 1] : 0.f));

@@ -61,19 +61,17 @@ __device__ __forceinline__ pair_t act_pair(pair_t z) {
   }
 }
 
+// The slope of GELU or SiLU.
 template <int ACT>
 __device__ __forceinline__ pair_t slope_pair(pair_t z) {
+  static_assert(ACT == kActGelu || ACT == kActSilu, "no slope of its own");
   if constexpr (ACT == kActGelu) {
     pair_t phi;
     const pair_t c = normal_cdf(z, &phi);
     return fma2(mul2(z, both(0.39894228f)), phi, c);
-  } else if constexpr (ACT == kActSilu) {
+  } else {
     const pair_t s = sigmoid(z);
     return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
-  } else if constexpr (ACT == kActRelu) {
-    return pair(lo(z) > 0.f ? 1.f : 0.f, hi(z) > 0.f ? 1.f : 0.f);
-  } else {
-    return both(1.f);
   }
 }
 

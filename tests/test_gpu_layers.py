@@ -219,6 +219,28 @@ def test_activation_extremes():
         assert torch.isnan(y[6, 0, 0]) and (act == "relu" or torch.isnan(s[6, 0, 0]))
 
 
+@pytest.mark.parametrize("shape", [(9, 8, 64, 1), (5, 8, 33, 1), (3, 8, 24, 16), (3, 8, 5, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_relu_drops_gradients_where_it_is_off(shape, dtype):
+    """An infinity or NaN in gy under an inactive unit reaches neither gz nor
+    gbias; under an active one it does, in its own channel only."""
+    P, _, C, N = shape
+    d = mqv.lin_desc(*shape, "relu")
+    rng = np.random.default_rng(11)
+    z, gy = rng.standard_normal((2, P, C, N)).astype(np.float32)
+    z[0, 0, 0], z[1, 1, 0], z[2, 2, 0], z[0, 3, 0] = -1.0, 0.0, -0.0, 1.0
+    plain = gy.copy()
+    gy[0, 0, 0], gy[1, 1, 0], gy[2, 2, 0] = np.inf, np.nan, -np.inf
+    plain[0, 0, 0] = plain[1, 1, 0] = plain[2, 2, 0] = 5.0
+    gz, gb = mqv.lin_act_grad(d, dev(gy, dtype), dev(z, BF16))
+    pz, pb = mqv.lin_act_grad(d, dev(plain, dtype), dev(z, BF16))
+    assert torch.isfinite(gz).all() and torch.equal(gz, pz) and torch.equal(gb, pb)
+    gy[0, 3, 0] = np.inf
+    gz, gb = mqv.lin_act_grad(d, dev(gy, dtype), dev(z, BF16))
+    assert torch.isinf(gz[0, 3, 0]) and (~torch.isfinite(gz)).sum() == 1
+    assert torch.isinf(gb[3]) and (~torch.isfinite(gb)).sum() == 1
+
+
 def test_linear_layer_of_nothing():
     for N in (1, 16):
         d = mqv.lin_desc(0, 24, 40, N, "gelu")
