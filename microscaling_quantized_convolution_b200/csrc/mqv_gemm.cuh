@@ -112,9 +112,19 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The whole warp waits; false if any lane gave up.
+// The whole warp waits, bounded as mbar_wait_bounded, and leaves as one: loads
+// and stores of tensor memory want all of its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, code));
+  constexpr long long kLimit = 1ll << 32;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xffffffffu, clock64() - t0 > kLimit)) {
+      atomicOr(err, code);
+      return false;
+    }
+  return true;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -382,10 +392,12 @@ __device__ __forceinline__ void stage_row(uint32_t tile, const GemmStaged<BF ? 2
 // tiles this warp has filled; `bars`: its two residual barriers; `acc`: the
 // barrier of the accumulator, waited for here; `bias_s`: 32 floats of the
 // warp's own shared memory; `release` is called once the accumulator is read.
+// 0, or if a wait gave up 1 + the residual loads, from `used` on, that it left
+// in flight.
 template <int COLS, bool BF, typename F>
-__device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const GemmMaps& maps, uint32_t tmem, uint32_t smem,
-                                                   int row0, int col0, int split, uint32_t& used, uint64_t* bars,
-                                                   uint64_t* acc, uint32_t acc_parity, float* bias_s, F release) {
+__device__ __forceinline__ int gemm_epilogue_fast(const GemmTcArgs& g, const GemmMaps& maps, uint32_t tmem, uint32_t smem,
+                                                  int row0, int col0, int split, uint32_t& used, uint64_t* bars,
+                                                  uint64_t* acc, uint32_t acc_parity, float* bias_s, F release) {
   const int lane = threadIdx.x & 31;
   const GemmStaged<BF ? 2 : 4> sy(g.col_chunk, lane);
   const GemmStaged<2> sz(g.col_chunk, lane);
@@ -419,7 +431,7 @@ __device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const Ge
       bulk_wait_read<1>();
     load_residual(c, used);
   }
-  if (!mbar_wait_bounded(acc, acc_parity, g.err, 4)) return false;
+  if (!warp_wait(acc, acc_parity, g.err, 4)) return 1 + (res && two);
   tc_fence_after();
   // not unrolled: the steps' code would not stay in the instruction cache
 #pragma unroll 1
@@ -469,7 +481,7 @@ __device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const Ge
     const uint32_t y = y_tile(used);
     if (res) {
       // barrier `used & 1` completes once every second step
-      if (!mbar_wait_bounded(bars + (used & 1), (used >> 1) & 1, g.err, 2)) return false;
+      if (!warp_wait(bars + (used & 1), (used >> 1) & 1, g.err, 2)) return 2 + (two && k + 32 < COLS);
 #pragma unroll
       for (int j = 0; j < (BF ? 4 : 8); ++j) {
         const uint4 t = ld_shared_v4(y + sy.off[j]);
@@ -494,7 +506,7 @@ __device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const Ge
     }
     c = nx;
   }
-  return true;
+  return 0;
 }
 
 // The tensor cores' running sum loses more than a rounding at each step: over
@@ -505,8 +517,9 @@ __device__ __forceinline__ bool gemm_epilogue_fast(const GemmTcArgs& g, const Ge
 // the last run's accumulator.  The tensor cores go on meanwhile with the other
 // accumulator.  Runs of 512 products: 4.8e-7 off over 8192, about what fp32
 // products on the CUDA cores are; runs of 1024: 9.9e-7, and 4 % faster (8192
-// tokens 4096 -> 4096, weight gradient: 203 and 196 us).  `tmem`: the first accumulator at the warp's lanes and columns;
-// `nt` counts the CTA's runs.  False if a wait gave up.
+// tokens 4096 -> 4096, weight gradient: 203 and 196 us).  `tmem`: the first
+// accumulator at the warp's lanes and columns; `nt` counts the CTA's runs.
+// False if a wait gave up.
 template <int BN, int COLS, typename F>
 __device__ __forceinline__ bool gemm_add_runs(const GemmTcArgs& g, uint32_t tmem, int runs, uint32_t& nt,
                                               uint64_t* acc_full, F release) {
@@ -515,7 +528,7 @@ __device__ __forceinline__ bool gemm_add_runs(const GemmTcArgs& g, uint32_t tmem
   for (int i = 0; i < COLS; ++i) sum[i] = 0.f;
   for (int run = 0; run < runs; ++run) {
     const int buf = nt & 1;
-    if (!mbar_wait_bounded(acc_full + buf, (nt / 2) & 1, g.err, 4)) return false;
+    if (!warp_wait(acc_full + buf, (nt / 2) & 1, g.err, 4)) return false;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < COLS; k += 32) {
@@ -757,15 +770,19 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
       auto release = [&] { release_buf(buf); };
       if constexpr (FAST) {
         const bool bf = !g.part && g.e.d.bf16;
-        if (!(bf ? gemm_epilogue_fast<BN / 2, true>(g, maps, acc, smem_u32(st), row0, tl.n * BN + c0, tl.split, used,
-                                                    res_full + 2 * (warp - 2), acc_full + buf, (nt / 2) & 1,
-                                                    bias_s + 32 * (warp - 2), release)
-                 : gemm_epilogue_fast<BN / 2, false>(g, maps, acc, smem_u32(st), row0, tl.n * BN + c0, tl.split, used,
-                                                     res_full + 2 * (warp - 2), acc_full + buf, (nt / 2) & 1,
-                                                     bias_s + 32 * (warp - 2), release)))
+        uint64_t* bars = res_full + 2 * (warp - 2);
+        float* bias = bias_s + 32 * (warp - 2);
+        const int col0 = tl.n * BN + c0;
+        const int gone = bf ? gemm_epilogue_fast<BN / 2, true>(g, maps, acc, smem_u32(st), row0, col0, tl.split, used, bars,
+                                                               acc_full + buf, (nt / 2) & 1, bias, release)
+                            : gemm_epilogue_fast<BN / 2, false>(g, maps, acc, smem_u32(st), row0, col0, tl.split, used, bars,
+                                                                acc_full + buf, (nt / 2) & 1, bias, release);
+        if (gone) {               // given up: the loads in flight still land in shared memory
+          for (uint32_t i = used; i < used + gone - 1; ++i) warp_wait(bars + (i & 1), (i >> 1) & 1, g.err, 2);
           break;
+        }
       } else {
-        if (!mbar_wait_bounded(acc_full + buf, (nt / 2) & 1, g.err, 4)) break;
+        if (!warp_wait(acc_full + buf, (nt / 2) & 1, g.err, 4)) break;
         tc_fence_after();
         gemm_epilogue_any<BN / 2>(g, acc, reinterpret_cast<float*>(st), row0, tl.n * BN + c0, tl.split, release);
       }
