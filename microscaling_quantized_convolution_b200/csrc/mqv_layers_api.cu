@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -72,7 +73,7 @@ mqv_status launched(const char* what) {
 }
 
 template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[kMaxDevices]) {
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -180,7 +181,7 @@ mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
 }
 
 template <typename K>
-cudaError_t launch_ln_kernel(K kernel, const LnArgs& a, const LnPlan& pl, int64_t smem, bool (&done)[kMaxDevices],
+cudaError_t launch_ln_kernel(K kernel, const LnArgs& a, const LnPlan& pl, int64_t smem, std::atomic<bool> (&done)[kMaxDevices],
                              cudaStream_t st) {
   const cudaError_t e = allow_smem(kernel, 200 * 1024, done);
   if (e != cudaSuccess) return e;
@@ -194,28 +195,28 @@ int64_t slot_bytes(const TensorIn& t, const LnPlan& pl, int depth) {
 
 template <bool VEC, int K, int T, int B, bool KEEP, bool EXACT = false>
 cudaError_t launch_ln_fwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP, EXACT>, a, pl, slot_bytes(a.x, pl, 3), done, st);
 }
 
 // The partial row is put together where the slots (or tiles' sums) were.
 template <bool VEC, int K, int T, int B, int D, bool EXACT = false>
 cudaError_t launch_ln_bwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   return launch_ln_kernel(ln_bwd_row_kernel<VEC, K, T, B, D, EXACT>, a, pl,
                           std::max(slot_bytes(a.x, pl, D) + slot_bytes(a.gy, pl, D), 2 * (int64_t)a.C * 4), done, st);
 }
 
 template <int V, int K, int T, bool EXACT = false>
 cudaError_t launch_ln_fwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, V);
   return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T, EXACT>, a, pl, sums, done, st);
 }
 
 template <int V, int K, int T, int B, bool EXACT = false>
 cudaError_t launch_ln_bwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, 2 * V);
   return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B, EXACT>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, st);
 }
@@ -299,7 +300,7 @@ mqv_status check_lin(const mqv_lin_desc* d) {
   // a position's columns are padded to whole chunks in the tiles
   const int64_t c = std::max(d->Cin, d->Cout), padded = d->N == 1 ? 1 : ceil_div(d->N, 64) * 64;
   if (c > (1 << 24) || d->N > kMaxColumns - 64 || d->P > kMaxColumns / padded ||
-      (d->P > 0 && c > kMaxElements / (d->P * padded)))
+      (d->P > 0 && c > kMaxElements / (d->P * padded)) || d->Cin > kMaxElements / d->Cout)
     return fail(MQV_ERR_UNSUPPORTED, "linear layer [%lld][%lld -> %lld][%lld] too large", (long long)d->P,
                 (long long)d->Cin, (long long)d->Cout, (long long)d->N);
   return MQV_OK;
@@ -581,7 +582,7 @@ mqv_status encode_output(CUtensorMap* map, const void* p, bool f32, const GemmTc
 
 template <int BN, bool PAIR, bool FAST, bool RUNS>
 cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
-  static bool done[kMaxDevices] = {};
+  static std::atomic<bool> done[kMaxDevices] = {};
   auto kernel = gemm_tc_kernel<BN, PAIR, FAST, RUNS>;
   const cudaError_t e = allow_smem(kernel, gemm_smem<BN, PAIR, FAST>, done);
   if (e != cudaSuccess) return e;

@@ -148,7 +148,8 @@ def lin_act_grad(gy, z, act):
         # most 1.5, each through at most 12 roundings, and |z|·exp(-z^2/2)
         # carries z^2/2 roundings of the exponent into a term below 1
         e_s = np.zeros_like(gy) if act == "relu" else np.full_like(gy, 16 * U)
-    gz = gy * slope
+    # relu selects: an infinite gy where it is off is dropped
+    gz = np.where(slope > 0, gy, 0.0) if act == "relu" else gy * slope
     e_gz = np.abs(gy) * e_s + U * np.abs(gz)
     return {"gz": (gz, e_gz),
             "gbias": (gz.sum((0, 2)), (column_adds(P * N) * U * np.abs(gz) + e_gz).sum((0, 2)))}

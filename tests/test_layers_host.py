@@ -118,6 +118,16 @@ def test_bad_lin_descriptors(kw):
     assert e.value.status in (1, 2)
 
 
+@pytest.mark.parametrize("op", [mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD, mqv.OP_ACT_GRAD])
+def test_weights_whose_tiles_pass_32_bits(op):
+    """More weights than an int counts tiles of are refused, whatever P is."""
+    for P, N in ((0, 1), (1, 1), (2, 4)):
+        with pytest.raises(mqv.MqvError) as e:
+            mqv.lin_workspace_bytes(mqv.lin_desc(P, 1 << 24, 1 << 24, N), op)
+        assert e.value.status in (1, 2)
+        assert mqv.lin_workspace_bytes(mqv.lin_desc(P, 1 << 20, 1 << 16, N), op) >= 0
+
+
 def test_reserved_fields_and_unknown_ops():
     d = mqv.lin_desc(4, 8, 8)
     with pytest.raises(mqv.MqvError):
