@@ -1,6 +1,8 @@
 """GPU parity of the layer norm and the linear layer against their fp64
 definitions, every output within the oracle's error bound, the same bits on a
 second run; streams, graphs, in-place forms, special values and refusals."""
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -371,6 +373,98 @@ def test_block_on_another_stream_and_in_a_graph(shape):
     fresh = _block(d1, d2, ln, t, x)
     for k in want:
         assert torch.equal(graphs[0][1][k], fresh[k]), k
+
+
+def test_block_from_several_host_threads():
+    """Threads with a stream each, calling at once, get what one alone gets."""
+    jobs = [_block_inputs(*shape, seed=i) for i, shape in enumerate(BLOCKS)]
+    want = [{k: v.clone() for k, v in _block(d1, d2, ln, t, x).items()} for t, x, d1, d2, ln in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        t, x, d1, d2, ln = jobs[i]
+        s = torch.cuda.Stream()
+        outs = [_block(d1, d2, ln, t, x, stream=s) for _ in range(8)]
+        s.synchronize()
+        return outs
+
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        for ref, outs in zip(want, pool.map(work, range(len(jobs)))):
+            for out in outs:
+                for k in ref:
+                    assert torch.equal(out[k], ref[k]), k
+    assert mqv.device_errors() == 0
+
+
+# ------------------------------------------------- offsets past 32 bits
+#
+# Tensors of more than 2^31 elements, zero but for their last positions: those
+# are checked against the definition, what lies before them against zero.
+
+def _tail(shape, k, rng, scale=1.0):
+    """(device tensor of zeros but for its last k positions, those as stored)."""
+    v = stored(rng.standard_normal((k, *shape[1:])) * scale, "bf16")
+    t = torch.zeros(shape, dtype=BF16, device="cuda")
+    t[-k:] = dev(v, BF16)
+    return t, v
+
+
+def _zero_before(t, k):
+    return not any(c.any() for c in t[:-k].split(1 << max(0, 28 - (t[0].numel() - 1).bit_length())))
+
+
+@pytest.mark.parametrize("shape", [(525000, 4096, 1), (2150000, 1001, 1), (33600, 1000, 64), (240000, 1001, 9)], ids=shape_id)
+def test_layer_norm_past_32_bits(shape):
+    P, C, N = shape
+    assert P * C * N > 1 << 31
+    rng, k = np.random.default_rng(5), 2
+    (x, xv), (gy, gyv) = _tail(shape, k, rng), _tail(shape, k, rng, 1e-2)
+    gamma = stored(rng.standard_normal(C) * 0.3 + 1, "f32")
+    d = mqv.ln_desc(P, C, N)
+    y, mean, rstd = mqv.ln_fwd(d, x, dev(gamma))
+    ref = L.ln_fwd(xv, gamma, None, EPS)
+    for got, name in ((y, "y"), (mean, "mean"), (rstd, "rstd")):
+        check(got[-k:], ref[name], name)
+    assert _zero_before(y, k) and _zero_before(mean, k)
+    gx, gg, gb = mqv.ln_bwd(d, gy, x, mean, rstd, dev(gamma), gx=y)
+    ref = L.ln_bwd(gyv, xv, mean[-k:].double().cpu().numpy(), rstd[-k:].double().cpu().numpy(), gamma)
+    check(gx[-k:], ref["gx"], "gx")
+    check(gg, ref["ggamma"], "ggamma")
+    check(gb, ref["gbeta"], "gbeta")
+    assert _zero_before(gx, k)
+
+
+@pytest.mark.parametrize("shape", [(2100000, 1024, 16, 1), (2150000, 1001, 24, 1), (33600, 1000, 8, 64),
+                                   (240000, 1001, 5, 9)], ids=shape_id)
+def test_linear_layer_past_32_bits(shape):
+    """Many inputs to few outputs, and the same few back to many."""
+    P, big, small, N = shape
+    assert P * big * N > 1 << 31
+    rng, k = np.random.default_rng(6), 2
+    x, xv = _tail((P, big, N), k, rng)
+    g, gv = _tail((P, small, N), k, rng)
+    w = stored(rng.standard_normal((small, big)) * 0.03, "bf16")
+    d = mqv.lin_desc(P, big, small, N)
+    y, _ = mqv.lin_fwd(d, dev(w, BF16), x, y_dtype=F32)
+    check(y[-k:], L.lin_fwd(w, xv, None, None, "none")["y"], "y")
+    assert _zero_before(y, k)
+    check(mqv.lin_wgrad(d, g, x), L.lin_wgrad(gv, xv)["gw"], "gw")
+    out = mqv.lin_dgrad(d, dev(w, BF16), g)
+    check(out[-k:], L.lin_dgrad(w, gv)["gx"], "gx")
+    assert _zero_before(out, k)
+    # the other way: x is the output side
+    d, wt = mqv.lin_desc(P, small, big, N, "relu"), np.ascontiguousarray(w.T)
+    out, _ = mqv.lin_fwd(d, dev(wt, BF16), g, residual=x, y=out)
+    check(out[-k:], L.lin_fwd(wt, gv, None, xv, "relu")["y"], "y")
+    assert _zero_before(out, k)
+    check(mqv.lin_wgrad(d, x, g), L.lin_wgrad(xv, gv)["gw"], "gw")
+    z = out
+    zv = z[-k:].double().cpu().numpy()
+    gz, gb = mqv.lin_act_grad(d, x, z, gz=x)
+    ref = L.lin_act_grad(xv, zv, "relu")
+    check(gz[-k:], ref["gz"], "gz")
+    check(gb, ref["gbias"], "gbias")
+    assert _zero_before(gz, k) and mqv.device_errors() == 0
 
 
 def test_given_workspaces_and_ragged_pointers():
