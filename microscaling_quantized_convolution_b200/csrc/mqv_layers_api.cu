@@ -256,7 +256,9 @@ cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStre
                     : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, st);
   }
   if (rows) {
-    if (pl.k == 4) return launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, st);
+    if (pl.k == 4)
+      return t <= 256 ? launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, st)
+                      : launch_ln_bwd_rows<false, 4, 512, 1, 1>(a, pl, st);
     return t <= 256   ? launch_ln_bwd_rows<false, 8, 256, 2, 1>(a, pl, st)
            : t <= 512 ? launch_ln_bwd_rows<false, 8, 512, 1, 1>(a, pl, st)
                       : launch_ln_bwd_rows<false, 8, 1024, 1, 1>(a, pl, st);

@@ -5,7 +5,10 @@ import torch
 # (P, C, N).  Token rows: one element, one token, widths that are no multiple
 # of a vector, the widths at which the vectors per thread change, the widest.
 LN_ROWS = [(1, 1, 1), (1, 8, 1), (3, 7, 1), (1, 1024, 1), (5, 1023, 1), (2, 2048, 1), (3, 2056, 1), (2, 4099, 1),
-           (300, 64, 1), (700, 136, 1), (2, 16384, 1), (1, 16383, 1), (1300, 264, 1)]
+           (300, 64, 1), (700, 136, 1), (2, 16384, 1), (1, 16383, 1), (1300, 264, 1),
+           # either side of each change of threads or of values a thread
+           (5, 255, 1), (5, 256, 1), (5, 257, 1), (3, 2047, 1), (700, 2049, 1), (4, 3001, 1), (2, 4095, 1), (3, 4096, 1),
+           (2, 4097, 1), (2, 4104, 1), (2, 8191, 1), (2, 8192, 1), (2, 8193, 1), (2, 8200, 1)]
 # Batch columns: one channel, odd batches, whole and ragged tiles of 64 batch
 # items, more channels than the widest tile takes, a large batch.
 LN_TILES = [(1, 1, 2), (3, 5, 3), (7, 64, 16), (4, 128, 64), (2, 512, 64), (2, 2048, 8), (1, 4096, 4), (1, 16384, 4),
