@@ -179,23 +179,33 @@ __device__ __forceinline__ void load_vectors(const TensorIn& t, int64_t i, int64
   }
 }
 
-// n single elements, `step` elements apart, zeros where the bit in `mask` is
-// not set.  The loads are unconditional, of the tensor's first element where
-// there is nothing to load, so that none waits for another.
+// n single elements, `step` elements apart, as they are stored.  The loads are
+// unconditional, of the tensor's first element where the bit in `mask` is not
+// set, so that none waits for another.
 template <int n>
-__device__ __forceinline__ void load_scalars(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, float (&f)[n]) {
+__device__ __forceinline__ void load_raw(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, uint32_t (&h)[n]) {
   if (t.bf16) {
-    uint16_t h[n];
 #pragma unroll
     for (int k = 0; k < n; ++k, i += step) h[k] = __ldg(static_cast<const uint16_t*>(t.p) + (mask >> k & 1 ? i : 0));
-#pragma unroll
-    for (int k = 0; k < n; ++k) f[k] = mask >> k & 1 ? __uint_as_float(static_cast<uint32_t>(h[k]) << 16) : 0.f;
   } else {
 #pragma unroll
-    for (int k = 0; k < n; ++k, i += step) f[k] = __ldg(static_cast<const float*>(t.p) + (mask >> k & 1 ? i : 0));
-#pragma unroll
-    for (int k = 0; k < n; ++k) f[k] = mask >> k & 1 ? f[k] : 0.f;
+    for (int k = 0; k < n; ++k, i += step) h[k] = __ldg(static_cast<const uint32_t*>(t.p) + (mask >> k & 1 ? i : 0));
   }
+}
+
+// Their values, zeros where the bit in `mask` is not set.
+template <int n>
+__device__ __forceinline__ void raw_values(const TensorIn& t, uint32_t mask, const uint32_t (&h)[n], float (&f)[n]) {
+  const int shift = t.bf16 ? 16 : 0;
+#pragma unroll
+  for (int k = 0; k < n; ++k) f[k] = mask >> k & 1 ? __uint_as_float(h[k] << shift) : 0.f;
+}
+
+template <int n>
+__device__ __forceinline__ void load_scalars(const TensorIn& t, int64_t i, int64_t step, uint32_t mask, float (&f)[n]) {
+  uint32_t h[n];
+  load_raw<n>(t, i, step, mask, h);
+  raw_values<n>(t, mask, h, f);
 }
 
 // A row thread's K vectors of 8, or 2·K scalars.
@@ -439,12 +449,31 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) ag[k][i] = ab[k][i] = 0;
+  // a row's statistics, and its scalars, are loaded a row ahead (8192 x 4096:
+  // 50 us, 55 without; 4097 x 1023: 15 and 20; 2000 x 4095: 24 and 36); not
+  // with sixteen scalars a thread, which leave no registers for it (2000 x
+  // 8191: 69 us, 64 without)
+  constexpr bool kStats = VEC || K <= 4, kAhead = !VEC && K <= 4;
+  constexpr int kRaw = kAhead ? 2 * K : 1;
+  float mean_next = 0.f, rstd_next = 0.f;
+  uint32_t x_next[kRaw], g_next[kRaw];
+  auto ahead = [&](int p) {
+    if (!kStats || p >= a.units) return;
+    mean_next = __ldg(a.mean + p);
+    rstd_next = __ldg(a.rstd + p);
+    if constexpr (kAhead) {
+      const int64_t at = static_cast<int64_t>(p) * C + c0;
+      load_raw<kRaw>(a.x, at, step, mask, x_next);
+      load_raw<kRaw>(a.gy, at, step, mask, g_next);
+    }
+  };
+  ahead(first);
   int turn = 0, odd = 0;
   for (int p = first; p < a.units; p += hop, odd ^= 1) {
     const int64_t at = static_cast<int64_t>(p) * C + c0;
     const uint32_t slot = s0 + turn * slot_bytes;
     turn = turn + 1 < D ? turn + 1 : 0;
-    const float mean = __ldg(a.mean + p), rstd = __ldg(a.rstd + p);
+    const float mean = kStats ? mean_next : __ldg(a.mean + p), rstd = kStats ? rstd_next : __ldg(a.rstd + p);
     pair_t x[K][V / 2], g[K][V / 2];
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -454,10 +483,19 @@ __global__ void __launch_bounds__(T, B) ln_bwd_row_kernel(const LnArgs a) {
       slot_wait<D>();
       slot_read<K>(a.x, mask, slot, x);
       slot_read<K>(a.gy, mask, slot + x_bytes, g);
+    } else if constexpr (kAhead) {
+      float f[kRaw];
+      raw_values<kRaw>(a.x, mask, x_next, f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k][0] = pair(f[2 * k], f[2 * k + 1]);
+      raw_values<kRaw>(a.gy, mask, g_next, f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) g[k][0] = pair(f[2 * k], f[2 * k + 1]);
     } else {
       load_all<VEC, V, K>(a.x, at, step, mask, x);
       load_all<VEC, V, K>(a.gy, at, step, mask, g);
     }
+    ahead(p + hop);
     const pair_t minus = pair(-mean, -mean), r2 = pair(rstd, rstd);
     pair_t t1 = 0, t2 = 0;
 #pragma unroll
