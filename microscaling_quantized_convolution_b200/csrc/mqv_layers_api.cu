@@ -430,18 +430,19 @@ GemmOperand operand_of(const GemmView& v, int rows, bool batch) {
 // times (us): `kBase` for launch, first loads and last epilogue, and for each
 // wave of tiles `start` and `block` for each K block, or `epilogue` where that
 // takes longer.  Measured (and modelled) for 8192 tokens, us in 256 x 256 tiles
-// of two CTAs, 128 x 128 and 128 x 64: 64 -> 4096 33, 31, 32 (33, 33, 35); 256
-// -> 4096 36, 36, 57 (34, 36, 60); 1024 -> 4096 57, 90, 154 (57, 90, 156); for
-// 2048 tokens 64 -> 1024 9.2, 6.5, 6.3 (8.6, 6.5, 6.7).  256 x 128 tiles of two
+// of two CTAs, 128 x 128 and 128 x 64: 64 -> 4096 34, 31, 32 (33, 33, 35); 256
+// -> 4096 36, 34, 53 (33, 33, 54); 1024 -> 4096 50, 78, 140 (50, 78, 140); for
+// 2048 tokens 64 -> 1024 9.6, 6.8, 6.0 (8.6, 6.5, 6.7).  256 x 128 tiles of two
 // CTAs were never faster than 128 x 128.  A split writes and reads fp32
-// partial sums and takes a second kernel.
+// partial sums and takes a second kernel (1024 tokens 2048 -> 128 in 128 x 64
+// tiles: split eight ways 9.9 us, four ways 10.1).
 void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
   struct Tile {
     int bn;
     bool pair;
     double start, block, epilogue;
   };
-  static constexpr Tile kTiles[] = {{256, true, 1.7, .36, 4.1}, {128, false, .95, .32, 2.0}, {64, false, .85, .285, 1.1}};
+  static constexpr Tile kTiles[] = {{256, true, 1.1, .34, 4.1}, {128, false, .8, .28, 2.0}, {64, false, .75, .255, 1.1}};
   constexpr double kBase = 4.5;
   double best = 0;
   for (const Tile& t : kTiles) {
@@ -452,7 +453,7 @@ void choose_tile(GemmPlan* pl, int64_t kblocks, int64_t vcols) {
       if (s > fill) continue;
       const double wave = std::max(t.start + ceil_div(kblocks, s) * t.block, t.epilogue);
       double us = kBase + ceil_div(tiles * s, units) * wave;
-      if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.0e6;
+      if (s > 1) us += 2.5 + s * pl->out_elems * 4 / 2.2e6;
       if (best == 0 || us < best) {
         best = us;
         pl->bn = t.bn;
