@@ -439,7 +439,8 @@ mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, con
 
 /* Linear layer Cin -> Cout over the channels of [P][Cin][N]: for tokens
  * (N = 1) y = x·w^T, for pixels a 1 x 1 convolution.  w: bfloat16
- * [Cout][Cin]; x and gz bfloat16 [P][Cin][N] and [P][Cout][N]. */
+ * [Cout][Cin]; x and gz bfloat16 [P][Cin][N] and [P][Cout][N].  At most 2^24
+ * channels on either side. */
 typedef struct {
   int64_t P, Cin, Cout, N;
   int32_t act;      /* mqv_act */

@@ -27,7 +27,7 @@
 // What bounds it: with many K blocks the operand bytes that come from L2 (a CTA
 // takes 32 KB a K block, about 0.32 us whatever the tile, so the pair's tile,
 // with twice the products for them, is the fast one: 8192 tokens 4096 -> 4096
-// in 170 us, 1.6 PFLOP/s, 0.95 of the measured bfloat16 rate); with few the
+// in 164 us, 1.67 PFLOP/s, 0.98 of the measured bfloat16 rate); with few the
 // epilogue (4 us for a 256 x 256 tile).
 //
 // Outputs.  FAST, when the output's rows are 16-byte aligned: an epilogue
@@ -517,7 +517,7 @@ __device__ __forceinline__ int gemm_epilogue_fast(const GemmTcArgs& g, const Gem
 // the last run's accumulator.  The tensor cores go on meanwhile with the other
 // accumulator.  Runs of 512 products: 4.8e-7 off over 8192, about what fp32
 // products on the CUDA cores are; runs of 1024: 9.9e-7, and 4 % faster (8192
-// tokens 4096 -> 4096, weight gradient: 203 and 196 us).  `tmem`: the first
+// tokens 4096 -> 4096, weight gradient: 196 and 188 us).  `tmem`: the first
 // accumulator at the warp's lanes and columns; `nt` counts the CTA's runs.
 // False if a wait gave up.
 template <int BN, int COLS, typename F>

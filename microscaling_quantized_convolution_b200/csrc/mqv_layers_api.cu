@@ -132,8 +132,8 @@ mqv_status plan_ln(const mqv_ln_desc* d, bool bwd, LnPlan* pl) {
   if (d->N == 1) {
     // 16 values per thread, which with their parameters (and backward the
     // parameters' gradients) is what registers hold at 512 to 768 threads an
-    // SM; 8 for short rows, and for scalars backward, which are not prefetched
-    // (4097 x 1023: 20 us against 21)
+    // SM; 8 for short rows, and for scalars backward, where the next row's then
+    // fit in registers too (4097 x 1023: 15 us against 21)
     pl->v = d->C % 8 == 0 ? 8 : 1;
     const int e = d->C <= 256 || (bwd && pl->v == 1 && d->C <= 4096) ? 8 : 16;
     pl->k = pl->v == 8 ? e / 8 : e / 2;
@@ -355,8 +355,8 @@ cudaError_t launch_act_grad(const ActGradArgs& a, const ActGradPlan& pl, int act
 }
 
 // A few tokens: the forward pass reads the weights once, without tiles.
-// (4096 -> 4096, us: 1 token 12, 4 tokens 15.5, 5 tokens in 128 x 128 tiles with K
-// split four ways 15.6; 1024 -> 1024: 4.4, 6.2 and 9.0.)
+// (4096 -> 4096, us: 1 token 12, 4 tokens 15.3, 5 tokens in tiles with K split
+// 15.8; 1024 -> 1024: 4.3, 6.3 and 8.6.)
 bool few_tokens(const mqv_lin_desc* d, int op) { return op == MQV_OP_FWD && d->N == 1 && d->P <= kFewTokens; }
 
 template <int P, bool ODD>

@@ -18,18 +18,19 @@
 // spread, arithmetic is on pairs (fma.rn.f32x2 and its kin: two IEEE
 // operations an instruction), and addresses are stepped, not multiplied.
 // Rows of vectors are on their way, D rows ahead (three, or one where
-// three do not fit), into slots of shared
-// memory that only the thread itself uses: loads stay in flight across the
-// reductions, and no barrier is needed for them.
+// three do not fit), into slots of shared memory that only the thread itself
+// uses: loads stay in flight across the reductions, and no barrier is needed
+// for them.  Scalars are loaded into registers a row ahead, where there are
+// some left.
 // The backward groups run over many rows or tiles and keep their channels'
 // parameter gradients in registers; a block adds its groups' in order and
 // writes one partial row, and column_sum_kernel adds the rows in a fixed order.
 //
 // Measured, L2 flushed: forward 16384 x 4096 bfloat16 47 us (5.7 TB/s, 0.89 of
 // the copy rate), 80 x 80 pixels of 64 channels at batch 16, fp32 to bfloat16,
-// 8.6 us (0.72); backward 8192 x 4096 54 us (3.7 TB/s, 0.57: instruction issue
+// 8.7 us (0.72); backward 8192 x 4096 50 us (4.0 TB/s, 0.62: instruction issue
 // and latency at the 512 threads an SM that the registers allow), 56 x 56
-// pixels of 128 channels at batch 64 in fp32 61 us (0.79), 28 x 28 20 us (2.65
+// pixels of 128 channels at batch 64 in fp32 60 us (0.79), 28 x 28 20 us (2.65
 // tiles a group: the last round is not full).  8 instead of 16 values a thread
 // at twice the threads are slower (64 us for 8192 x 4096 backward), so are 80
 // registers for a third block (76 us, spills), or a prefetch of tiles (no gain).
