@@ -313,6 +313,7 @@ struct ActGradPlan {
   unsigned gx, gy;
 };
 
+// For P > 0: the element limit then keeps the blocks below a grid's limit.
 ActGradPlan plan_act_grad(const mqv_lin_desc* d) {
   ActGradPlan pl = {};
   int64_t steps;
@@ -682,6 +683,7 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
 
 int64_t lin_ws(const mqv_lin_desc* d, int op) {
   if (op == MQV_OP_ACT_GRAD) {
+    if (d->P == 0) return 0;
     const ActGradPlan pl = plan_act_grad(d);
     return align256((int64_t)pl.gy * pl.tiles * d->Cout * 4);
   }
@@ -822,7 +824,7 @@ mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_ty
                           "gz", "gy")))
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const ActGradPlan pl = plan_act_grad(d);
+  const ActGradPlan pl = cols > 0 ? plan_act_grad(d) : ActGradPlan{};
   ActGradArgs a = {};
   a.gy = {gy, gy_type == MQV_BF16};
   a.z = act ? z : nullptr;
@@ -838,7 +840,7 @@ mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_ty
     const cudaError_t e = launch_act_grad(a, pl, d->act, s);
     if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
   }
-  if (gbias) launch_column_sum(a.part, cols > 0 ? (int64_t)pl.gy * pl.tiles : 0, d->Cout, 1, gbias, nullptr, s);
+  if (gbias) launch_column_sum(a.part, (int64_t)pl.gy * pl.tiles, d->Cout, 1, gbias, nullptr, s);
   return launched("activation gradient launch");
 }
 

@@ -2,6 +2,8 @@
 central differences and against torch's fp64 autograd, workspace sizes, and
 every refusal of the C ABI and the binding, which come before any launch."""
 import ctypes
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ import torch
 import microscaling_quantized_convolution_b200 as mqv
 from microscaling_quantized_convolution_b200 import build as mqv_build
 from oracle import layers_oracle as L
+from tests.conftest import ROOT
 from tests.layers_cases import LIN_LONG, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES
 
 
@@ -231,6 +234,17 @@ def test_empty_calls_launch_nothing():
     d = mqv.ln_desc(0, 64, 1)
     assert _ln_fwd(d, x=None, y=None, mean=None, rstd=None) == 0
     assert _lin_fwd(mqv.lin_desc(0, 8, 8), x=None, res=None, z=None, y=None) == 0
+
+
+@pytest.mark.parametrize("N", [1, 2048, 1 << 20, 1 << 28])
+def test_activation_gradient_of_nothing_needs_no_plan(N):
+    """P = 0 has no element limit, so C and N together may pass any grid's:
+    the workspace query answers 0 (asked in a process of its own, which an
+    arithmetic trap would end)."""
+    code = ("import microscaling_quantized_convolution_b200 as m; "
+            f"print(m.lin_workspace_bytes(m.lin_desc(0, 1, 1 << 24, {N}, 'gelu'), m.OP_ACT_GRAD))")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert run.returncode == 0 and run.stdout.strip() == "0", (run.returncode, run.stdout, run.stderr[-500:])
 
 
 def test_binding_refuses_cpu_tensors():
