@@ -462,8 +462,8 @@ mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, cons
 /* gz = gy·act'(z), rounded to bfloat16, and gbias[co] = sum_{p,n} of the
  * unrounded gz.  (The residual's gradient is gy.)  For MQV_ACT_RELU gz is gy
  * where z > 0 and 0 elsewhere, whatever gy is there.  z: as mqv_lin_fwd kept it,
- * not read when act is MQV_ACT_NONE; gz or gbias may be NULL, not both; gz
- * may be gy itself when gy is bfloat16. */
+ * not read when act is MQV_ACT_NONE; gz or gbias may be NULL, not both unless
+ * P = 0; gz may be gy itself when gy is bfloat16. */
 mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_type, const void* z, void* gz,
                             float* gbias, void* ws, size_t ws_bytes, void* stream);
 

@@ -812,7 +812,8 @@ mqv_status mqv_lin_act_grad(const mqv_lin_desc* d, const void* gy, int32_t gy_ty
   mqv_status st = check_lin(d);
   if (st || (st = check_type(gy_type, "gy"))) return st;
   const int64_t cols = d->P * d->N, n = cols * d->Cout;
-  if (!gz && !gbias) return fail(MQV_ERR_INVALID_ARG, "gz and gbias: one at least");
+  if (!gz && !gbias)             // nothing to write: the rule only where there is something, as empty tensors are null
+    return cols > 0 ? fail(MQV_ERR_INVALID_ARG, "gz and gbias: one at least") : ok();
   const int64_t need = gbias ? lin_ws(d, MQV_OP_ACT_GRAD) : 0;
   if ((st = check_workspace(ws, ws_bytes, need))) return st;
   const bool act = d->act != MQV_ACT_NONE;

@@ -254,6 +254,14 @@ def test_linear_layer_of_nothing():
         assert y.shape == (0, 40, N) and gx.shape == (0, 24, N) and not gb.any() and not gw.any()
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_activation_gradient_of_nothing_alone(act):
+    g = torch.empty((0, 40, 16), device="cuda")
+    z = g.to(BF16)
+    gz, gb = mqv.lin_act_grad(mqv.lin_desc(0, 24, 40, 16, act), g, z, bias_grad=False)
+    assert gz.shape == g.shape and gz.dtype == BF16 and gb is None
+
+
 def test_linear_layer_residual_in_place():
     for shape in ((70, 128, 136, 1), (5, 64, 48, 16), (1, 64, 200, 1)):
         w, x, bias, res, _ = lin_inputs(shape)

@@ -247,6 +247,14 @@ def test_activation_gradient_of_nothing_needs_no_plan(N):
     assert run.returncode == 0 and run.stdout.strip() == "0", (run.returncode, run.stdout, run.stderr[-500:])
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_activation_gradient_of_nothing_without_a_bias_gradient(act):
+    """An empty tensor has a null pointer, so with P = 0 neither gz nor gbias
+    need be there; nothing is launched.  With positions, one is needed."""
+    assert _lin_act_grad(mqv.lin_desc(0, 8, 8, 1, act), gy=None, z=None, gz=None, gb=None, ws=None, wsn=0) == 0
+    assert _lin_act_grad(mqv.lin_desc(1, 8, 8, 1, act), gz=None, gb=None) == INVALID
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(4, 64)
     h = x.to(torch.bfloat16)
