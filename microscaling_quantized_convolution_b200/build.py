@@ -30,13 +30,16 @@ def _headers():
 
 def _object_deps(src):
     """The files of this tree that the object was compiled from, as nvcc wrote
-    them down beside it; every header where it has not."""
+    them down beside it; every header where it has not, was cut off, or wrote
+    them down for another place that this tree was copied from."""
+    path = os.path.join(CSRC, src)
     try:
         with open(_object(src)[:-2] + ".d") as f:
-            words = f.read().split(":", 1)[1].replace("\\\n", " ").split()
+            words = f.read().partition(":")[2].replace("\\\n", " ").split()
     except OSError:
-        return [os.path.join(CSRC, src)] + _headers()
-    return [w for w in map(os.path.realpath, words) if w.startswith(os.path.realpath(ROOT) + os.sep)]
+        words = []
+    deps = [w for w in map(os.path.realpath, words) if w.startswith(os.path.realpath(ROOT) + os.sep)]
+    return deps if os.path.realpath(path) in deps else [path] + _headers()
 
 
 def _stale(out, deps):
