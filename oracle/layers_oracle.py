@@ -57,9 +57,18 @@ def act_slope(z: np.ndarray, act: str) -> np.ndarray:
     return np.ones_like(z)
 
 
-# additions per term of a sum over the channels: 16 in a thread, 5 across a
-# warp, 5 across warps (10 over channel rows), and the final factor 1/C
-_CHANNEL_ADDS = 32
+def channel_adds(C: int, N: int) -> int:
+    """Roundings per term of a mean over the C channels of a [P][C][N] tensor,
+    1/C's own and the product with it (2) among them.
+    Rows (N = 1): 16 values in a thread, 5 additions across a warp, 5 across
+    the warps: 15 + 5 + 5 + 2 < 32.
+    Tiles: up to 16 values in a thread; then, where the tile's lanes divide no
+    warp, halvings of up to 1024 rows, 15 + 10 + 2 < 32.  Where they do, 5 at
+    most across the warp, and the warps' sums one after another: a thread
+    holds 8 channels at 4 batch items of a tile of 64 at most (16 lanes), or
+    16 channels at one of 32 lanes at most, so there are C / 16 warps and a
+    part of one at most, and no more than 32: 15 + 5 + min(32, C / 16 + 1) + 2."""
+    return 32 if N == 1 else max(32, 22 + min(32, C // 16 + 1))
 
 
 def ln_fwd(x, gamma, beta, eps):
@@ -73,19 +82,29 @@ def ln_fwd(x, gamma, beta, eps):
     var = (xc * xc).mean(1, keepdims=True)
     rstd = (var + eps) ** -0.5
     y = xc * rstd * g + b
-    e_mean = _CHANNEL_ADDS * U * np.abs(x).mean(1, keepdims=True)
+    adds = channel_adds(C, x.shape[2])
+    e_mean = adds * U * np.abs(x).mean(1, keepdims=True)
     e_xc = e_mean + U * np.abs(xc)
     # d var: the sum's own error, and 2|xc|·e_xc per term; rstd = (var + eps)^-1/2
-    e_var = (_CHANNEL_ADDS + 2) * U * var + (2 * np.abs(xc) * e_xc + e_xc * e_xc).mean(1, keepdims=True)
+    e_var = (adds + 2) * U * var + (2 * np.abs(xc) * e_xc + e_xc * e_xc).mean(1, keepdims=True)
     e_rstd = rstd * (0.5 * e_var / (var + eps) + 4 * U)
     e_y = np.abs(g) * (e_xc * (rstd + e_rstd) + np.abs(xc) * e_rstd) + 3 * U * (np.abs(y) + np.abs(b))
     return {"y": (y, e_y), "mean": (mean[:, 0], e_mean[:, 0]), "rstd": (rstd[:, 0], e_rstd[:, 0])}
 
 
 def column_adds(units: int) -> int:
-    """Additions per term of a parameter gradient: at least 148 blocks share
-    the rows or tiles (`units`), 8 values of one at most go into a sum; 8
-    lanes, then the blocks' partial rows in 8 parts."""
+    """Additions per term of a parameter gradient, at most.
+    Layer norm: 148 blocks or all `units` share the rows or tiles, and one of
+    them takes a thread's sum through 4 additions at most (4 batch items);
+    then the block's groups and, where no shuffles add them (5), the lanes of
+    each in turn, 256 together, since a block that has several groups has 256
+    threads; then up to 296 blocks' rows in 32 parts, 10 and 5:
+    4·ceil(units / 148) + 256 + 15.
+    Activation gradient, up to 8192 channels: a thread adds its positions,
+    P·N / 18 at most (1184 blocks or four positions a block; a block has 256
+    threads along N, or 8 rows of tokens), then 8 elements, 256 threads, and
+    up to 1184 rows and their batch tiles in 32 parts, 37 and 5.
+    Both are below the sum here."""
     return 8 * (-(-units // 148) + 1) + 64 + 148 * 32 // 8 + 8
 
 
@@ -100,8 +119,9 @@ def ln_bwd(gy, x, mean, rstd, gamma):
     m1, m2 = g.mean(1, keepdims=True), (g * xh).mean(1, keepdims=True)
     a1, a2 = np.abs(g).mean(1, keepdims=True), np.abs(g * xh).mean(1, keepdims=True)
     gx = rstd * (g - m1 - xh * m2)
-    e1 = (_CHANNEL_ADDS + 2) * U * a1
-    e2 = (_CHANNEL_ADDS + 4) * U * a2
+    adds = channel_adds(C, N)
+    e1 = (adds + 2) * U * a1
+    e2 = (adds + 4) * U * a2
     e_gx = rstd * (e1 + np.abs(xh) * e2 + e_xh * (np.abs(m2) + e2)
                    + 4 * U * (np.abs(g) + np.abs(m1) + np.abs(xh * m2))) + 2 * U * np.abs(gx)
     D = column_adds(P * N)

@@ -131,6 +131,25 @@ def test_layer_norm_special_columns(shape):
         check(y[:, :, 1:].contiguous(), ref["y"], "y")
 
 
+@pytest.mark.parametrize("shape,rows,per_warp", [((1, 16384, 4), 1024, 32), ((1, 4096, 8), 512, 16)])
+def test_layer_norm_sums_take_no_more_additions_than_bounded(shape, rows, per_warp):
+    """A one, and in every place where a partial sum that holds it takes
+    another addend 2^-24, which a sum of 1 loses whole: a thread's channels
+    are `rows` apart, a warp holds `per_warp` neighbouring rows.  The mean is
+    off by as many of them as a term goes through additions, which the
+    oracle's bound counts."""
+    P, C, N = shape
+    x = np.zeros(shape)
+    x[:, 0] = 1.0
+    x[:, rows::rows] = 2.0 ** -24                              # within a thread
+    x[:, [1 << i for i in range(per_warp.bit_length() - 1)]] = 2.0 ** -24      # across the warp
+    x[:, per_warp:rows:per_warp] = 2.0 ** -24                  # across the warps
+    y, mean, rstd = mqv.ln_fwd(mqv.ln_desc(*shape), dev(x))
+    ref = L.ln_fwd(x, None, None, EPS)
+    for got, name in ((mean, "mean"), (rstd, "rstd"), (y, "y")):
+        check(got, ref[name], name)
+
+
 def test_layer_norm_of_nothing():
     for N in (1, 16):
         d = mqv.ln_desc(0, 64, N)
