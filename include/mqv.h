@@ -492,6 +492,14 @@ mqv_status mqv_device_errors(uint32_t* flags, void* stream);
  * MQV_ERR_TIMEOUT with that bit.  Not part of the method. */
 mqv_status mqv_selftest_wait_timeout(int64_t limit_cycles, void* stream);
 
+/* Test hooks: the kernel instances, as text, that mqv_ln_fwd (bwd = 0) or
+ * mqv_ln_bwd, or a product of the linear layer (op = MQV_OP_FWD, MQV_OP_WGRAD
+ * or MQV_OP_DGRAD; out_type: of y or gx), would launch for the descriptor;
+ * empty for P = 0.  Host-only: with them the tests show that their shapes
+ * reach every instance.  Not part of the method. */
+mqv_status mqv_selftest_ln_instance(const mqv_ln_desc* d, int32_t bwd, char* text, size_t bytes);
+mqv_status mqv_selftest_lin_instance(const mqv_lin_desc* d, int32_t op, int32_t out_type, char* text, size_t bytes);
+
 #ifdef __cplusplus
 }
 #endif

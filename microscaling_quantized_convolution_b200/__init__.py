@@ -166,6 +166,10 @@ _SIGS = {
                                      ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "mqv_lin_wgrad": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mqv_selftest_ln_instance": (ctypes.c_int, [ctypes.POINTER(LnDesc), ctypes.c_int32, ctypes.c_char_p,
+                                                ctypes.c_size_t]),
+    "mqv_selftest_lin_instance": (ctypes.c_int, [ctypes.POINTER(LinDesc), ctypes.c_int32, ctypes.c_int32,
+                                                 ctypes.c_char_p, ctypes.c_size_t]),
 }
 
 
@@ -935,3 +939,18 @@ def lin_wgrad(d: LinDesc, gz: torch.Tensor, x: torch.Tensor, gw: torch.Tensor | 
         ws, wp, wn = _layer_ws(ws, need, at)
         _check(lib().mqv_lin_wgrad(ctypes.byref(d), gp, xp, gw.data_ptr(), wp, wn, _raw_stream(dev)))
     return gw
+
+
+def selftest_ln_instance(d: LnDesc, bwd: bool = False) -> str:
+    """Test hook: the kernel instance that ln_fwd or ln_bwd would launch."""
+    text = ctypes.create_string_buffer(256)
+    _check(lib().mqv_selftest_ln_instance(ctypes.byref(d), int(bwd), text, len(text)))
+    return text.value.decode()
+
+
+def selftest_lin_instance(d: LinDesc, op: int, dtype=torch.bfloat16) -> str:
+    """Test hook: the kernel instances that lin_fwd, lin_wgrad or lin_dgrad (op)
+    with results of `dtype` would launch."""
+    text = ctypes.create_string_buffer(256)
+    _check(lib().mqv_selftest_lin_instance(ctypes.byref(d), op, _TYPES[dtype], text, len(text)))
+    return text.value.decode()

@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdarg>
+#include <cstdio>
 #include <initializer_list>
 
 #include "mqv.h"
@@ -71,6 +73,21 @@ mqv_status launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ok() : cuda_fail(e, what);
 }
+
+// Where a pass goes: to a stream or, for the test hooks, into the text of the
+// kernel instances that it would launch.
+struct Target {
+  cudaStream_t st;
+  char* text;                  // null: launch
+  size_t size;
+  __attribute__((format(printf, 2, 3))) cudaError_t name(const char* fmt, ...) const {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(text, size, fmt, ap);
+    va_end(ap);
+    return cudaSuccess;
+  }
+};
 
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
@@ -194,81 +211,85 @@ int64_t slot_bytes(const TensorIn& t, const LnPlan& pl, int depth) {
 }
 
 template <bool VEC, int K, int T, int B, bool KEEP, bool EXACT = false>
-cudaError_t launch_ln_fwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+cudaError_t launch_ln_fwd_rows(const LnArgs& a, const LnPlan& pl, const Target& to) {
+  if (to.text) return to.name("launch_ln_fwd_rows<%d, %d, %d, %d, %d, %d>", VEC, K, T, B, KEEP, EXACT);
   static std::atomic<bool> done[kMaxDevices] = {};
-  return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP, EXACT>, a, pl, slot_bytes(a.x, pl, 3), done, st);
+  return launch_ln_kernel(ln_fwd_row_kernel<VEC, K, T, B, 3, KEEP, EXACT>, a, pl, slot_bytes(a.x, pl, 3), done, to.st);
 }
 
 // The partial row is put together where the slots (or tiles' sums) were.
 template <bool VEC, int K, int T, int B, int D, bool EXACT = false>
-cudaError_t launch_ln_bwd_rows(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+cudaError_t launch_ln_bwd_rows(const LnArgs& a, const LnPlan& pl, const Target& to) {
+  if (to.text) return to.name("launch_ln_bwd_rows<%d, %d, %d, %d, %d, %d>", VEC, K, T, B, D, EXACT);
   static std::atomic<bool> done[kMaxDevices] = {};
   return launch_ln_kernel(ln_bwd_row_kernel<VEC, K, T, B, D, EXACT>, a, pl,
-                          std::max(slot_bytes(a.x, pl, D) + slot_bytes(a.gy, pl, D), 2 * (int64_t)a.C * 4), done, st);
+                          std::max(slot_bytes(a.x, pl, D) + slot_bytes(a.gy, pl, D), 2 * (int64_t)a.C * 4), done, to.st);
 }
 
 template <int V, int K, int T, bool EXACT = false>
-cudaError_t launch_ln_fwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+cudaError_t launch_ln_fwd_tiles(const LnArgs& a, const LnPlan& pl, const Target& to) {
+  if (to.text) return to.name("launch_ln_fwd_tiles<%d, %d, %d, %d>", V, K, T, EXACT);
   static std::atomic<bool> done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, V);
-  return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T, EXACT>, a, pl, sums, done, st);
+  return launch_ln_kernel(ln_fwd_tile_kernel<V, K, T, EXACT>, a, pl, sums, done, to.st);
 }
 
 template <int V, int K, int T, int B, bool EXACT = false>
-cudaError_t launch_ln_bwd_tiles(const LnArgs& a, const LnPlan& pl, cudaStream_t st) {
+cudaError_t launch_ln_bwd_tiles(const LnArgs& a, const LnPlan& pl, const Target& to) {
+  if (to.text) return to.name("launch_ln_bwd_tiles<%d, %d, %d, %d, %d>", V, K, T, B, EXACT);
   static std::atomic<bool> done[kMaxDevices] = {};
   const int64_t sums = (int64_t)pl.groups * 2 * 4 * tile_sum_floats(pl.lanes, pl.group, 2 * V);
-  return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B, EXACT>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, st);
+  return launch_ln_kernel(ln_bwd_tile_kernel<V, K, T, B, EXACT>, a, pl, std::max(sums, 2 * (int64_t)a.C * 4), done, to.st);
 }
 
 // Instances: EXACT ones for the usual widths, the others for the rest.
-cudaError_t launch_ln_fwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+cudaError_t launch_ln_fwd(const LnArgs& a, const LnPlan& pl, bool rows, const Target& to) {
   const int t = pl.threads();
   if (rows && pl.v == 8) {
-    if (pl.k == 1) return launch_ln_fwd_rows<true, 1, 128, 6, true>(a, pl, st);
+    if (pl.k == 1) return launch_ln_fwd_rows<true, 1, 128, 6, true>(a, pl, to);
     if (t <= 256)
-      return pl.exact ? launch_ln_fwd_rows<true, 2, 256, 3, true, true>(a, pl, st)
-                      : launch_ln_fwd_rows<true, 2, 256, 3, true>(a, pl, st);
-    return t <= 512 ? launch_ln_fwd_rows<true, 2, 512, 1, true>(a, pl, st)
-                    : launch_ln_fwd_rows<true, 2, 1024, 1, false>(a, pl, st);
+      return pl.exact ? launch_ln_fwd_rows<true, 2, 256, 3, true, true>(a, pl, to)
+                      : launch_ln_fwd_rows<true, 2, 256, 3, true>(a, pl, to);
+    return t <= 512 ? launch_ln_fwd_rows<true, 2, 512, 1, true>(a, pl, to)
+                    : launch_ln_fwd_rows<true, 2, 1024, 1, false>(a, pl, to);
   }
   if (rows) {
-    if (pl.k == 4) return launch_ln_fwd_rows<false, 4, 128, 6, true>(a, pl, st);
-    return t <= 256   ? launch_ln_fwd_rows<false, 8, 256, 3, true>(a, pl, st)
-           : t <= 512 ? launch_ln_fwd_rows<false, 8, 512, 1, true>(a, pl, st)
-                      : launch_ln_fwd_rows<false, 8, 1024, 1, false>(a, pl, st);
+    if (pl.k == 4) return launch_ln_fwd_rows<false, 4, 128, 6, true>(a, pl, to);
+    return t <= 256   ? launch_ln_fwd_rows<false, 8, 256, 3, true>(a, pl, to)
+           : t <= 512 ? launch_ln_fwd_rows<false, 8, 512, 1, true>(a, pl, to)
+                      : launch_ln_fwd_rows<false, 8, 1024, 1, false>(a, pl, to);
   }
   if (pl.v == 4) {
-    if (t > 512) return launch_ln_fwd_tiles<4, 8, 1024>(a, pl, st);
-    return pl.exact ? launch_ln_fwd_tiles<4, 8, 512, true>(a, pl, st) : launch_ln_fwd_tiles<4, 8, 512>(a, pl, st);
+    if (t > 512) return launch_ln_fwd_tiles<4, 8, 1024>(a, pl, to);
+    return pl.exact ? launch_ln_fwd_tiles<4, 8, 512, true>(a, pl, to) : launch_ln_fwd_tiles<4, 8, 512>(a, pl, to);
   }
-  return t <= 512 ? launch_ln_fwd_tiles<1, 16, 512>(a, pl, st) : launch_ln_fwd_tiles<1, 16, 1024>(a, pl, st);
+  return t <= 512 ? launch_ln_fwd_tiles<1, 16, 512>(a, pl, to) : launch_ln_fwd_tiles<1, 16, 1024>(a, pl, to);
 }
 
-cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, cudaStream_t st) {
+cudaError_t launch_ln_bwd(const LnArgs& a, const LnPlan& pl, bool rows, const Target& to) {
   const int t = pl.threads();
   if (rows && pl.v == 8) {
-    if (pl.k == 1) return launch_ln_bwd_rows<true, 1, 256, 2, 3>(a, pl, st);
+    if (pl.k == 1) return launch_ln_bwd_rows<true, 1, 256, 2, 3>(a, pl, to);
     if (t <= 256)
-      return pl.exact ? launch_ln_bwd_rows<true, 2, 256, 2, 3, true>(a, pl, st)
-                      : launch_ln_bwd_rows<true, 2, 256, 2, 3>(a, pl, st);
-    return t <= 512 ? launch_ln_bwd_rows<true, 2, 512, 1, 3>(a, pl, st)
-                    : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, st);
+      return pl.exact ? launch_ln_bwd_rows<true, 2, 256, 2, 3, true>(a, pl, to)
+                      : launch_ln_bwd_rows<true, 2, 256, 2, 3>(a, pl, to);
+    return t <= 512 ? launch_ln_bwd_rows<true, 2, 512, 1, 3>(a, pl, to)
+                    : launch_ln_bwd_rows<true, 2, 1024, 1, 1>(a, pl, to);
   }
   if (rows) {
     if (pl.k == 4)
-      return t <= 256 ? launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, st)
-                      : launch_ln_bwd_rows<false, 4, 512, 1, 1>(a, pl, st);
-    return t <= 256   ? launch_ln_bwd_rows<false, 8, 256, 2, 1>(a, pl, st)
-           : t <= 512 ? launch_ln_bwd_rows<false, 8, 512, 1, 1>(a, pl, st)
-                      : launch_ln_bwd_rows<false, 8, 1024, 1, 1>(a, pl, st);
+      return t <= 256 ? launch_ln_bwd_rows<false, 4, 256, 2, 1>(a, pl, to)
+                      : launch_ln_bwd_rows<false, 4, 512, 1, 1>(a, pl, to);
+    // from 4097 channels on: 288 threads or more
+    return t <= 512 ? launch_ln_bwd_rows<false, 8, 512, 1, 1>(a, pl, to)
+                    : launch_ln_bwd_rows<false, 8, 1024, 1, 1>(a, pl, to);
   }
   if (pl.v == 4) {
-    if (t > 512) return launch_ln_bwd_tiles<4, 8, 1024, 1>(a, pl, st);
-    if (t > 256) return launch_ln_bwd_tiles<4, 8, 512, 1>(a, pl, st);
-    return pl.exact ? launch_ln_bwd_tiles<4, 8, 256, 2, true>(a, pl, st) : launch_ln_bwd_tiles<4, 8, 256, 2>(a, pl, st);
+    if (t > 512) return launch_ln_bwd_tiles<4, 8, 1024, 1>(a, pl, to);
+    if (t > 256) return launch_ln_bwd_tiles<4, 8, 512, 1>(a, pl, to);
+    return pl.exact ? launch_ln_bwd_tiles<4, 8, 256, 2, true>(a, pl, to) : launch_ln_bwd_tiles<4, 8, 256, 2>(a, pl, to);
   }
-  return t <= 512 ? launch_ln_bwd_tiles<1, 16, 512, 1>(a, pl, st) : launch_ln_bwd_tiles<1, 16, 1024, 1>(a, pl, st);
+  return t <= 512 ? launch_ln_bwd_tiles<1, 16, 512, 1>(a, pl, to) : launch_ln_bwd_tiles<1, 16, 1024, 1>(a, pl, to);
 }
 
 LnArgs ln_args(const mqv_ln_desc* d, const LnPlan& pl, const void* x, int32_t x_type, const float* gamma) {
@@ -361,24 +382,29 @@ cudaError_t launch_act_grad(const ActGradArgs& a, const ActGradPlan& pl, int act
 bool few_tokens(const mqv_lin_desc* d, int op) { return op == MQV_OP_FWD && d->N == 1 && d->P <= kFewTokens; }
 
 template <int P, bool ODD>
-cudaError_t launch_few_tokens_p(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, cudaStream_t st) {
+cudaError_t launch_few_tokens_p(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, const Target& to) {
   constexpr int R = P <= 2 ? 1 : 2;                // rows a warp, which share the tokens' loads
+  if (to.text) return to.name("few_tokens_kernel<%d, %d, %d>", P, R, ODD);
   // warps to a row, so that a lane's eight loads at a time are all it has
   int split = 1;
   while (split < kFewThreads / 32 && d->Cin > split * 256 * (8 / R)) split *= 2;
-  few_tokens_kernel<P, R, ODD><<<(unsigned)ceil_div(d->Cout, R * (kFewThreads / 32 / split)), kFewThreads, 0, st>>>(
+  few_tokens_kernel<P, R, ODD><<<(unsigned)ceil_div(d->Cout, R * (kFewThreads / 32 / split)), kFewThreads, 0, to.st>>>(
       e, static_cast<const uint16_t*>(w), static_cast<const uint16_t*>(x), (int)d->Cin, (int)d->Cout, split);
   return cudaGetLastError();
 }
 
 template <bool ODD>
-cudaError_t launch_few_tokens(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, cudaStream_t st) {
+cudaError_t launch_few_tokens_odd(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, const Target& to) {
   switch (d->P) {
-    case 1: return launch_few_tokens_p<1, ODD>(d, e, w, x, st);
-    case 2: return launch_few_tokens_p<2, ODD>(d, e, w, x, st);
-    case 3: return launch_few_tokens_p<3, ODD>(d, e, w, x, st);
-    default: return launch_few_tokens_p<4, ODD>(d, e, w, x, st);
+    case 1: return launch_few_tokens_p<1, ODD>(d, e, w, x, to);
+    case 2: return launch_few_tokens_p<2, ODD>(d, e, w, x, to);
+    case 3: return launch_few_tokens_p<3, ODD>(d, e, w, x, to);
+    default: return launch_few_tokens_p<4, ODD>(d, e, w, x, to);
   }
+}
+
+cudaError_t launch_few_tokens(const mqv_lin_desc* d, const Epilogue& e, const void* w, const void* x, const Target& to) {
+  return d->Cin % 8 == 0 ? launch_few_tokens_odd<false>(d, e, w, x, to) : launch_few_tokens_odd<true>(d, e, w, x, to);
 }
 
 // ---- products on the tensor cores
@@ -585,7 +611,11 @@ mqv_status encode_output(CUtensorMap* map, const void* p, bool f32, const GemmTc
 }
 
 template <int BN, bool PAIR, bool FAST, bool RUNS>
-cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
+cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, const Target& to) {
+  if (to.text)
+    return to.name("gemm_tc_kernel<%d, %d, %d, %d>%s%s%s", BN, PAIR, FAST, RUNS,
+                   pl.args.splits == 1 ? "" : pl.args.e.vec4 ? " split_sum_kernel<4>" : " split_sum_kernel<1>",
+                   pl.a.copied() ? " copy a" : "", pl.b.copied() ? " copy b" : "");
   static std::atomic<bool> done[kMaxDevices] = {};
   auto kernel = gemm_tc_kernel<BN, PAIR, FAST, RUNS>;
   const cudaError_t e = allow_smem(kernel, gemm_smem<BN, PAIR, FAST>, done);
@@ -596,7 +626,7 @@ cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStrea
   cfg.gridDim = (unsigned)(std::min<int64_t>(tiles, kSms / kCtas) * kCtas);
   cfg.blockDim = kGemmThreads;
   cfg.dynamicSmemBytes = gemm_smem<BN, PAIR, FAST>;
-  cfg.stream = st;
+  cfg.stream = to.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCtas;
@@ -607,10 +637,22 @@ cudaError_t launch_gemm_tile(const GemmPlan& pl, const GemmMaps& maps, cudaStrea
 }
 
 template <bool FAST, bool RUNS>
-cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, cudaStream_t st) {
-  if (pl.pair) return launch_gemm_tile<256, true, FAST, RUNS>(pl, maps, st);
-  return pl.bn == 128 ? launch_gemm_tile<128, false, FAST, RUNS>(pl, maps, st)
-                      : launch_gemm_tile<64, false, FAST, RUNS>(pl, maps, st);
+cudaError_t launch_gemm_form(const GemmPlan& pl, const GemmMaps& maps, const Target& to) {
+  if (pl.pair) return launch_gemm_tile<256, true, FAST, RUNS>(pl, maps, to);
+  return pl.bn == 128 ? launch_gemm_tile<128, false, FAST, RUNS>(pl, maps, to)
+                      : launch_gemm_tile<64, false, FAST, RUNS>(pl, maps, to);
+}
+
+// Rows of whole 16-byte vectors, in bfloat16 too: outputs go by TMA.
+bool fast_output(const GemmPlan& pl) { return pl.args.col_inner % 8 == 0; }
+
+// Results kept in fp32: runs of 512 products, else one run.
+int run_length(const GemmPlan& pl, bool bf16) { return bf16 ? pl.args.kblocks : 8; }
+
+cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, const Target& to) {
+  const bool runs = ceil_div(pl.args.kblocks, pl.args.splits) > pl.args.run;
+  if (fast_output(pl)) return runs ? launch_gemm_form<true, true>(pl, maps, to) : launch_gemm_form<true, false>(pl, maps, to);
+  return runs ? launch_gemm_form<false, true>(pl, maps, to) : launch_gemm_form<false, false>(pl, maps, to);
 }
 
 // Copies an operand whose rows are unaligned to its place in the workspace.
@@ -640,8 +682,7 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
   g.e = e;
   g.e.vec4 = plan_e.vec4;
   g.e.bias_on_row = plan_e.bias_on_row;
-  // results kept in fp32: runs of 512 products, else one run
-  g.run = g.e.d.bf16 ? g.kblocks : 8;
+  g.run = run_length(pl, g.e.d.bf16);
   char* w = static_cast<char*>(ws);
   if (g.splits > 1) g.part = reinterpret_cast<float*>(w);
   w += pl.part_bytes;
@@ -654,18 +695,14 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
   if ((s = encode_operand(&maps.a, ta, pl.a, pl.oa, kGemmBM)) ||
       (s = encode_operand(&maps.b, tb, pl.b, pl.ob, pl.pair ? pl.bn / 2 : pl.bn)))
     return s;
-  // rows of whole 16-byte vectors, in bfloat16 too: outputs go by TMA
-  const bool fast = g.col_inner % 8 == 0;
-  if (fast) {
+  if (fast_output(pl)) {
     if ((s = encode_output(&maps.d, g.part ? g.part : g.e.d.p, g.part || !g.e.d.bf16, g))) return s;
     if (!g.part && g.e.z.p && (s = encode_output(&maps.z, g.e.z.p, false, g))) return s;
     if (!g.part && g.e.residual && (s = encode_output(&maps.residual, g.e.residual, !g.e.d.bf16, g))) return s;
   }
   repitch(pl.a, a, ta, st);
   repitch(pl.b, b, tb, st);
-  const bool runs = ceil_div(g.kblocks, g.splits) > g.run;
-  const cudaError_t ce = fast ? (runs ? launch_gemm<true, true>(pl, maps, st) : launch_gemm<true, false>(pl, maps, st))
-                              : (runs ? launch_gemm<false, true>(pl, maps, st) : launch_gemm<false, false>(pl, maps, st));
+  const cudaError_t ce = launch_gemm(pl, maps, {st, nullptr, 0});
   if (ce != cudaSuccess) return cuda_fail(ce, "linear layer launch");
   if (g.splits > 1) {
     const int64_t inner = g.e.bias_on_row ? g.col_inner : 1, channels = g.e.bias_on_row ? pl.M : g.col_inner;
@@ -718,7 +755,7 @@ mqv_status mqv_ln_fwd(const mqv_ln_desc* d, const void* x, int32_t x_type, const
   a.mean = mean;
   a.rstd = rstd;
   a.out = {y, y_type == MQV_BF16};
-  const cudaError_t e = launch_ln_fwd(a, pl, d->N == 1, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_ln_fwd(a, pl, d->N == 1, {static_cast<cudaStream_t>(stream), nullptr, 0});
   return e == cudaSuccess ? ok() : cuda_fail(e, "layer norm launch");
 }
 
@@ -761,7 +798,7 @@ mqv_status mqv_ln_bwd(const mqv_ln_desc* d, const void* gy, int32_t gy_type, con
   a.out = {gx, gx_type == MQV_BF16};
   a.part = ggamma ? static_cast<float*>(ws) : nullptr;
   if (cols > 0) {
-    const cudaError_t e = launch_ln_bwd(a, pl, d->N == 1, s);
+    const cudaError_t e = launch_ln_bwd(a, pl, d->N == 1, {s, nullptr, 0});
     if (e != cudaSuccess) return cuda_fail(e, "layer norm gradient launch");
   }
   if (ggamma) launch_column_sum(a.part, pl.blocks, d->C, 2, ggamma, gbeta, s);
@@ -800,8 +837,7 @@ mqv_status mqv_lin_fwd(const mqv_lin_desc* d, const void* w, const void* x, cons
   e.bias = bias;
   e.act = d->act;
   if (few_tokens(d, MQV_OP_FWD) && cols > 0) {
-    const cudaError_t ce = d->Cin % 8 == 0 ? launch_few_tokens<false>(d, e, w, x, static_cast<cudaStream_t>(stream))
-                                           : launch_few_tokens<true>(d, e, w, x, static_cast<cudaStream_t>(stream));
+    const cudaError_t ce = launch_few_tokens(d, e, w, x, {static_cast<cudaStream_t>(stream), nullptr, 0});
     return ce == cudaSuccess ? ok() : cuda_fail(ce, "linear layer launch");
   }
   return run_gemm(d, MQV_OP_FWD, d->N == 1 ? x : w, d->N == 1 ? w : x, e, ws, static_cast<cudaStream_t>(stream));
@@ -875,6 +911,36 @@ mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, f
   Epilogue e = {};
   e.d = {gw, 0};
   return run_gemm(d, MQV_OP_WGRAD, gz, x, e, ws, static_cast<cudaStream_t>(stream));
+}
+
+mqv_status mqv_selftest_ln_instance(const mqv_ln_desc* d, int32_t bwd, char* text, size_t bytes) {
+  LnPlan pl;
+  const mqv_status st = plan_ln(d, bwd != 0, &pl);
+  if (st) return st;
+  if (!text || !bytes) return fail(MQV_ERR_INVALID_ARG, "null output buffer");
+  const Target to = {nullptr, text, bytes};
+  text[0] = 0;
+  if (d->P > 0) (bwd ? launch_ln_bwd : launch_ln_fwd)(LnArgs{}, pl, d->N == 1, to);
+  return ok();
+}
+
+mqv_status mqv_selftest_lin_instance(const mqv_lin_desc* d, int32_t op, int32_t out_type, char* text, size_t bytes) {
+  mqv_status st = check_lin(d);
+  if (st || (st = check_type(out_type, "output"))) return st;
+  if (op != MQV_OP_FWD && op != MQV_OP_WGRAD && op != MQV_OP_DGRAD) return fail(MQV_ERR_INVALID_ARG, "unknown op %d", op);
+  if (!text || !bytes) return fail(MQV_ERR_INVALID_ARG, "null output buffer");
+  const Target to = {nullptr, text, bytes};
+  text[0] = 0;
+  if (d->P == 0) return ok();
+  if (few_tokens(d, op)) {
+    launch_few_tokens(d, Epilogue{}, nullptr, nullptr, to);
+  } else {
+    GemmPlan pl;
+    plan_gemm(d, op, &pl);
+    pl.args.run = run_length(pl, out_type == MQV_BF16 && op != MQV_OP_WGRAD);
+    launch_gemm(pl, GemmMaps{}, to);
+  }
+  return ok();
 }
 
 }  // extern "C"

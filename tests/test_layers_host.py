@@ -2,6 +2,8 @@
 central differences and against torch's fp64 autograd, workspace sizes, and
 every refusal of the C ABI and the binding, which come before any launch."""
 import ctypes
+import os
+import re
 import subprocess
 import sys
 
@@ -145,6 +147,47 @@ def test_reserved_fields_and_unknown_ops():
     assert mqv.lib().mqv_lin_workspace_size(None, mqv.OP_FWD, None) == 1
     assert mqv.lib().mqv_lin_workspace_size(ctypes.byref(mqv.lin_desc(4, 8, 8)), mqv.OP_FWD, None) == 1
     assert mqv.lib().mqv_ln_bwd_workspace_size(ctypes.byref(mqv.ln_desc(4, 8)), None) == 1
+
+
+# ------------------------------------------------------- kernel instances
+
+def _ln_instances():
+    """The instances that the dispatch can launch, from its source, as the test
+    hook names them (the last parameter, EXACT, is false where not given)."""
+    params = {"launch_ln_fwd_rows": 6, "launch_ln_bwd_rows": 6, "launch_ln_fwd_tiles": 4, "launch_ln_bwd_tiles": 5}
+    with open(os.path.join(mqv_build.CSRC, "mqv_layers_api.cu")) as f:
+        calls = re.findall(r"(launch_ln_\w+)<([\w, ]+)>\(a, pl, to\)", f.read())
+    out = set()
+    for name, args in calls:
+        args = [{"true": "1", "false": "0"}.get(a, a) for a in args.split(", ")]
+        out.add(f"{name}<{', '.join(args + ['0'] * (params[name] - len(args)))}>")
+    assert len(out) > 20
+    return out
+
+
+def test_every_layer_norm_instance_is_for_some_shape():
+    reached = set()
+    for N in (1, 2, 3, 4, 8, 12, 16, 64):
+        for C in range(1, 16385, 1 if N == 1 else 61 if N > 4 else 97):
+            reached |= {mqv.selftest_ln_instance(mqv.ln_desc(2, c, N), bwd) for c in {C, min(16384, -(-C // 64) * 64)}
+                        for bwd in (False, True)}
+    assert reached == _ln_instances()
+
+
+def test_instance_hooks_refuse_what_the_calls_refuse():
+    assert mqv.selftest_ln_instance(mqv.ln_desc(0, 64)) == "" == mqv.selftest_lin_instance(mqv.lin_desc(0, 8, 8), mqv.OP_FWD)
+    with pytest.raises(mqv.MqvError):
+        mqv.selftest_ln_instance(mqv.ln_desc(1, 16385))
+    with pytest.raises(mqv.MqvError):
+        mqv.selftest_lin_instance(mqv.lin_desc(1, 0, 8), mqv.OP_FWD)
+    with pytest.raises(mqv.MqvError):
+        mqv.selftest_lin_instance(mqv.lin_desc(1, 8, 8), mqv.OP_ACT_GRAD)
+    text = ctypes.create_string_buffer(b"untouched", 12)
+    assert mqv.lib().mqv_selftest_ln_instance(ctypes.byref(mqv.ln_desc(1, 8)), 0, text, 0) == 1
+    assert mqv.lib().mqv_selftest_ln_instance(ctypes.byref(mqv.ln_desc(1, 8)), 0, None, 12) == 1
+    assert text.value == b"untouched"
+    assert mqv.lib().mqv_selftest_ln_instance(ctypes.byref(mqv.ln_desc(1, 8)), 0, text, 4) == 0
+    assert text.value == b"lau"                                   # cut off within its size
 
 
 # addresses of pretend buffers, far enough apart for the shapes used here;
