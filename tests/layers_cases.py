@@ -23,11 +23,31 @@ LIN_PIXELS = [(1, 3, 5, 2), (7, 16, 8, 4), (49, 64, 64, 16), (5, 33, 40, 12), (4
               (10, 24, 24, 8), (3, 40, 48, 32), (2, 16, 16, 200), (6, 65, 63, 16), (1, 128, 128, 96), (30, 64, 128, 24),
               (1, 200, 72, 7), (100, 16, 24, 16), (2, 136, 320, 128), (9, 48, 72, 20), (5, 64, 64, 40),
               (1, 72, 64, 256)]
-# enough tiles for two-CTA tiles of 256 x 256 or 256 x 128 in one pass or another
+# enough tiles for tiles of 128 x 128 in one pass or another
 LIN_WIDE = [(2500, 40, 1992, 1), (2300, 72, 2047, 1), (1300, 64, 1608, 1), (65, 1992, 2500, 1), (600, 264, 280, 16),
             (300, 264, 520, 32), (150, 260, 264, 64), (150, 264, 296, 80)]
 # contractions longer than one accumulator's run, K not split to shorter ones
 LIN_LONG = [(1280, 1100, 1000, 1), (1270, 1100, 1003, 1), (90, 1000, 1100, 8)]
+# two-CTA tiles of 256 x 256 in one pass at least: output rows that end on, just
+# past and just short of 128 and 256, with and without whole vectors to a row,
+# sums in one run and in several, K split and whole, copied operands
+LIN_PAIR = [(245, 520, 1248, 4), (285, 1049, 803, 4), (238, 656, 760, 8), (300, 585, 739, 8),
+            (41, 1936, 1736, 4), (513, 3778, 546, 1), (541, 3728, 552, 1), (596, 531, 3752, 1),
+            (181, 1993, 267, 4), (311, 193, 1843, 4), (174, 400, 1952, 4), (332, 152, 2040, 8),
+            (134, 2456, 3168, 1), (557, 544, 3736, 1), (144, 3096, 2552, 1), (138, 2553, 3256, 1),
+            (2125, 1028, 544, 1), (2308, 136, 3943, 1), (1153, 584, 1884, 1), (572, 582, 3876, 1),
+            (18, 2033, 1267, 7), (19, 1160, 1968, 8), (26, 1768, 1376, 7), (1082, 129, 515, 8),
+            (264, 583, 3812, 1), (39, 1873, 1211, 7), (257, 960, 2523, 1), (257, 2048, 1184, 1),
+            (36, 1184, 1936, 8), (257, 2243, 1152, 1), (1152, 2376, 263, 1), (5, 1505, 1715, 64),
+            (478, 1648, 152, 8), (61, 1209, 1923, 8), (2449, 136, 3520, 1), (513, 2352, 1004, 1),
+            (2848, 133, 3248, 1), (2570, 3076, 161, 1)]
+# up to four tokens: whole and odd rows, more channels than one warp's loads take
+LIN_FEW = [(1, 5, 7, 1), (1, 2056, 40, 1), (1, 4099, 33, 1), (2, 7, 5, 1), (2, 1001, 1003, 1), (2, 4104, 24, 1),
+           (3, 24, 41, 1), (3, 2048, 96, 1), (3, 4099, 33, 1), (4, 5, 7, 1), (4, 136, 72, 1), (4, 1003, 1001, 1),
+           (4, 4096, 520, 1)]
+# either side of the change to 1024 threads a tile
+LN_WIDE_TILES = [(2, 1024, 16), (2, 1025, 16), (4, 1500, 16), (4, 2048, 16), (3, 2000, 12), (5, 1100, 12), (2, 1400, 12),
+                 (300, 1032, 16)]
 
 
 def shape_id(s):

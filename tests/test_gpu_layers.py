@@ -9,7 +9,8 @@ import torch
 
 import microscaling_quantized_convolution_b200 as mqv
 from oracle import layers_oracle as L
-from tests.layers_cases import LIN_LONG, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES, activations, shape_id, stored
+from tests.layers_cases import (LIN_FEW, LIN_LONG, LIN_PAIR, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES,
+                                LN_WIDE_TILES, activations, shape_id, stored)
 
 pytestmark = pytest.mark.gpu
 
@@ -71,6 +72,12 @@ def test_layer_norm(shape, xt, yt):
     gx2, gg2, gb2 = mqv.ln_bwd(d, gyd, xd, mean2, rstd2, gd, gx_dtype=gxt)
     for a, b in ((y, y2), (mean, mean2), (rstd, rstd2), (gx, gx2), (gg, gg2), (gb, gb2)):
         assert torch.equal(a, b.view(a.shape))
+
+
+@pytest.mark.parametrize("xt,yt", TYPES, ids=["f32-f32", "f32-bf16", "bf16-bf16", "bf16-f32"])
+@pytest.mark.parametrize("shape", LN_WIDE_TILES, ids=shape_id)
+def test_layer_norm_on_wide_tiles(shape, xt, yt):
+    test_layer_norm(shape, xt, yt)
 
 
 @pytest.mark.parametrize("shape", [(9, 264, 1), (9, 33, 1), (5, 24, 16), (3, 20, 12)], ids=shape_id)
@@ -195,6 +202,11 @@ def test_linear_layer(shape):
     check(gw, L.lin_wgrad(gz, x)["gw"], "gw")
     assert torch.equal(gx, mqv.lin_dgrad(d, wd, gzd)) and torch.equal(gw, mqv.lin_wgrad(d, gzd, xd))
     assert mqv.device_errors() == 0
+
+
+@pytest.mark.parametrize("shape", LIN_PAIR + LIN_FEW, ids=shape_id)
+def test_linear_layer_in_pairs_and_of_few_tokens(shape):
+    test_linear_layer(shape)
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])

@@ -15,7 +15,8 @@ import microscaling_quantized_convolution_b200 as mqv
 from microscaling_quantized_convolution_b200 import build as mqv_build
 from oracle import layers_oracle as L
 from tests.conftest import ROOT
-from tests.layers_cases import LIN_LONG, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES
+from tests.layers_cases import (LIN_FEW, LIN_LONG, LIN_PAIR, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES,
+                                LN_WIDE_TILES)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -172,6 +173,39 @@ def test_every_layer_norm_instance_is_for_some_shape():
             reached |= {mqv.selftest_ln_instance(mqv.ln_desc(2, c, N), bwd) for c in {C, min(16384, -(-C // 64) * 64)}
                         for bwd in (False, True)}
     assert reached == _ln_instances()
+
+
+def test_gpu_shapes_reach_every_layer_norm_instance():
+    reached = {mqv.selftest_ln_instance(mqv.ln_desc(*s), bwd) for s in LN_ROWS + LN_TILES + LN_WIDE_TILES
+               for bwd in (False, True)}
+    assert reached == _ln_instances()
+
+
+def test_gpu_shapes_reach_every_product_instance():
+    """Every tile, with outputs by TMA and without, in one run of K and in
+    several, whole and split; the pair's tile in each pass, for tokens and for
+    pixels.  A change of the tile model that moves them fails here."""
+    reached, passes = set(), set()
+    for s in LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG + LIN_PAIR + LIN_FEW:
+        for op in (mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD):
+            for t in (torch.float32, torch.bfloat16):
+                name = mqv.selftest_lin_instance(mqv.lin_desc(*s), op, t)
+                reached.add(name.replace(" copy a", "").replace(" copy b", ""))
+                if "gemm_tc_kernel<256" in name:
+                    passes.add((name.split(">")[0], "split" in name, op, s[3] > 1))
+    for p, r in ((1, 1), (2, 1), (3, 2), (4, 2)):
+        assert {f"few_tokens_kernel<{p}, {r}, {odd}>" for odd in (0, 1)} <= reached
+    for tile in ("64, 0", "128, 0", "256, 1"):
+        for fast in (0, 1):
+            for runs in (0, 1):
+                assert f"gemm_tc_kernel<{tile}, {fast}, {runs}>" in reached, (tile, fast, runs)
+                assert any(f"gemm_tc_kernel<{tile}, {fast}, {runs}> split_sum_kernel<{v}>" in reached for v in (1, 4))
+    for op in (mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD):
+        for pixels in (False, True):
+            for fast in (0, 1):
+                for runs in (0, 1):
+                    assert any((f"gemm_tc_kernel<256, 1, {fast}, {runs}", split, op, pixels) in passes
+                               for split in (False, True)), (op, pixels, fast, runs)
 
 
 def test_instance_hooks_refuse_what_the_calls_refuse():
