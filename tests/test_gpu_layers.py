@@ -209,6 +209,37 @@ def test_linear_layer_in_pairs_and_of_few_tokens(shape):
     test_linear_layer(shape)
 
 
+def _integers(shape, limit, g):
+    return torch.randint(-limit, limit + 1, shape, generator=g, device="cuda").to(BF16)
+
+
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG + LIN_PAIR + LIN_FEW, ids=shape_id)
+def test_products_of_integers_are_exact(shape):
+    """Small integers: every sum of products, in any order, is an integer below
+    2^24 that fp32 holds (9 times at most 12500 terms), so the results have one
+    value, and a product left out or taken twice shows."""
+    P, Cin, Cout, N = shape
+    assert 9 * max(Cin, Cout, P * N) + 100 < 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    w, x, gz = _integers((Cout, Cin), 3, g), _integers((P, Cin, N), 3, g), _integers((P, Cout, N), 3, g)
+    bias, res = _integers((Cout,), 50, g).float(), _integers((P, Cout, N), 50, g)
+    d = mqv.lin_desc(*shape)
+    # columns as rows: plain matrices, fp64
+    xm, gm = (t.double().transpose(1, 2).reshape(P * N, -1) for t in (x, gz))
+    rows = lambda t: t.double().transpose(1, 2).reshape(P * N, -1)  # noqa: E731
+    zr = xm @ w.double().t()
+    for dtype in (F32, BF16):
+        y, z = mqv.lin_fwd(d, w, x, y=poison((P, Cout, N), dtype), save_z=True)
+        assert torch.equal(rows(y), zr.to(dtype).double()) and torch.equal(rows(z), zr.to(BF16).double())
+        y, _ = mqv.lin_fwd(d, w, x, bias=bias, residual=res.to(dtype))
+        assert torch.equal(rows(y), (zr + bias.double() + rows(res)).to(dtype).double())
+        gx = mqv.lin_dgrad(d, w, gz, gx=poison((P, Cin, N), dtype))
+        assert torch.equal(rows(gx), (gm @ w.double()).to(dtype).double())
+    gw = mqv.lin_wgrad(d, gz, x, gw=poison((Cout, Cin), F32))
+    assert torch.equal(gw.double(), gm.t() @ xm)
+    assert mqv.device_errors() == 0
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 9, 1), (5, 1003, 1), (300, 64, 1), (2100, 520, 1), (3, 5, 2),
                                    (49, 64, 16), (40, 33, 12), (600, 24, 64), (5, 3, 84), (2, 2, 5000), (3, 7, 2056)],
