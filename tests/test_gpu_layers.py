@@ -561,6 +561,61 @@ def test_given_workspaces_and_ragged_pointers():
         mqv.lin_fwd(d, wd, big[4:])
 
 
+def _guarded(call, need, kind):
+    """call(ws) with a workspace of exactly `need` bytes between guard bytes,
+    all of them NaN patterns: the same result as with the call's own, twice
+    (the second time over what the first left), the guards untouched; a
+    shorter and a misaligned one are refused."""
+    assert need > 0 and need % 256 == 0, kind
+    want = [t.clone() for t in call(None)]
+    buf = torch.full((need + 2048,), 255, dtype=torch.uint8, device="cuda")
+    ws = buf[1024:1024 + need]
+    for _ in range(2):
+        got = call(ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True)), kind
+        assert (buf[:1024] == 255).all() and (buf[1024 + need:] == 255).all(), kind
+    for bad in (buf[1024:1024 + need - 1], buf[1032:1032 + need]):
+        with pytest.raises(mqv.MqvError):
+            call(bad)
+
+
+FWD, WGRAD, DGRAD = mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD
+
+
+@pytest.mark.parametrize("shape,ops", [
+    # K split, whole vectors
+    ((64, 4096, 256, 1), (FWD,)), ((4100, 136, 72, 1), (WGRAD,)), ((500, 520, 136, 16), (WGRAD,)),
+    # copies of operands with unaligned rows
+    ((129, 257, 255, 1), (FWD, WGRAD, DGRAD)), ((90, 1003, 1001, 1), (FWD, WGRAD, DGRAD)),
+    # both, in one tile or another
+    ((33, 3001, 257, 1), (FWD, WGRAD, DGRAD)), ((2570, 3076, 161, 1), (FWD, WGRAD, DGRAD)),
+    ((70, 2000, 136, 7), (FWD, WGRAD, DGRAD)), ((200, 1992, 72, 12), (FWD, WGRAD, DGRAD)),
+    ((600, 128, 136, 20), (FWD, WGRAD, DGRAD))], ids=str)
+def test_product_workspaces_of_their_exact_size(shape, ops):
+    P, Cin, Cout, N = shape
+    w, x, bias, res, gy = lin_inputs(shape)
+    wd, xd, bd, rd, gd = dev(w, BF16), dev(x, BF16), dev(bias), dev(res), dev(gy, BF16)
+    d = mqv.lin_desc(*shape, "silu")
+    calls = {FWD: lambda ws: mqv.lin_fwd(d, wd, xd, bias=bd, residual=rd, save_z=True, ws=ws),
+             DGRAD: lambda ws: (mqv.lin_dgrad(d, wd, gd, ws=ws),), WGRAD: lambda ws: (mqv.lin_wgrad(d, gd, xd, ws=ws),)}
+    for op in ops:
+        _guarded(calls[op], mqv.lin_workspace_bytes(d, op), (shape, op))
+    assert mqv.device_errors() == 0
+
+
+@pytest.mark.parametrize("shape", [(5, 1023, 1), (700, 136, 1), (3, 20, 12), (4, 128, 64), (2, 2048, 16), (1, 1, 1)],
+                         ids=shape_id)
+def test_gradient_workspaces_of_their_exact_size(shape):
+    P, C, N = shape
+    x, gamma, _, gy = ln_inputs(shape)
+    xd, gd, gyd = dev(x), dev(gamma), dev(gy)
+    ln, lin = mqv.ln_desc(*shape), mqv.lin_desc(P, 8, C, N, "gelu")
+    _, mean, rstd = mqv.ln_fwd(ln, xd, gd)
+    _guarded(lambda ws: mqv.ln_bwd(ln, gyd, xd, mean, rstd, gd, ws=ws), mqv.ln_bwd_workspace_bytes(ln), shape)
+    z = xd.to(BF16)
+    _guarded(lambda ws: mqv.lin_act_grad(lin, gyd, z, ws=ws), mqv.lin_workspace_bytes(lin, mqv.OP_ACT_GRAD), shape)
+
+
 def test_binding_refusals():
     d, ln = mqv.lin_desc(4, 16, 24, 1, "gelu"), mqv.ln_desc(4, 16)
     w = torch.zeros((24, 16), dtype=BF16, device="cuda")
