@@ -74,7 +74,7 @@ struct GemmTcArgs {
   GemmOperand a, b;
   int tiles_m, tiles_n, splits, kblocks;
   int tail_width;              // N tiles of the last band (see gemm_tile)
-  int run;                     // K blocks summed by one accumulator (see gemm_add_runs)
+  int run;                     // K blocks summed by one accumulator at most (see gemm_add_runs)
   FastDiv by_split, by_band, by_tail, by_pos;   // divisions by tiles of a split, of a band, tail_width, col_per_pos
   // output element (row, column c of chunk q = c / col_chunk):
   //   (q / col_per_pos)·pos + row·row_stride + (q % col_per_pos)·col_chunk + c % col_chunk
@@ -509,15 +509,18 @@ __device__ __forceinline__ int gemm_epilogue_fast(const GemmTcArgs& g, const Gem
   return 0;
 }
 
-// The tensor cores' running sum loses more than a rounding at each step: over
-// 1400 products it is off by 1.4e-6 (2-norm, of operands whose channels have
-// offsets), and more the longer it runs.  Results that are kept in fp32 are
-// therefore summed in runs of g.run K blocks; the epilogue warps add the runs'
-// sums in registers, rounding to nearest, and put the total in the place of
-// the last run's accumulator.  The tensor cores go on meanwhile with the other
-// accumulator.  Runs of 512 products: 4.8e-7 off over 8192, about what fp32
-// products on the CUDA cores are; runs of 1024: 9.9e-7, and 4 % faster (8192
-// tokens 4096 -> 4096, weight gradient: 196 and 188 us).  `tmem`: the first
+// The tensor cores' running sum truncates: each step of 16 products loses up
+// to a step of the sum, 2·2^-24, and always towards zero, so the loss grows with
+// the length (positive products, mean loss in units of 2^-24 of the sum: 512
+// 1.8, 1024 11, 4096 169, 8192 504; 2-norm of the error on noise 4.7e-7, 1.0e-6,
+// 4.4e-6, 9.1e-6).  Sums are therefore made in runs of g.run K blocks; the
+// epilogue warps add the runs' sums in registers, rounding to nearest, and put
+// the total in the place of the last run's accumulator.  The tensor cores go
+// on meanwhile with the other accumulator.  Results kept in fp32, runs of 512
+// products: 4.8e-7 off over any length, three to four times what fp32 products
+// rounded to nearest are for a few hundred; runs of 1024: 9.9e-7, and 4 %
+// faster (8192 tokens 4096 -> 4096, weight gradient: 196 and 188 us).  Results
+// in bfloat16, runs of 32768.  `tmem`: the first
 // accumulator at the warp's lanes and columns; `nt` counts the CTA's runs.
 // False if a wait gave up.
 template <int BN, int COLS, typename F>

@@ -646,8 +646,13 @@ cudaError_t launch_gemm_form(const GemmPlan& pl, const GemmMaps& maps, const Tar
 // Rows of whole 16-byte vectors, in bfloat16 too: outputs go by TMA.
 bool fast_output(const GemmPlan& pl) { return pl.args.col_inner % 8 == 0; }
 
-// Results kept in fp32: runs of 512 products, else one run.
-int run_length(const GemmPlan& pl, bool bf16) { return bf16 ? pl.args.kblocks : 8; }
+// K blocks that an accumulator sums at most (see gemm_add_runs): 512 products
+// for results kept in fp32, 32768 for bfloat16 ones, whose sums then lose a
+// sixteenth of their rounding at most (in one run of 262144 positive products,
+// half of it).  A tile whose sum takes two runs does not have its epilogue
+// under the next tile's products: in runs of 16384, 2048 tokens 32768 -> 2048
+// took 241 us, 225 in one.
+int run_length(bool bf16) { return bf16 ? 512 : 8; }
 
 cudaError_t launch_gemm(const GemmPlan& pl, const GemmMaps& maps, const Target& to) {
   const bool runs = ceil_div(pl.args.kblocks, pl.args.splits) > pl.args.run;
@@ -682,7 +687,7 @@ mqv_status run_gemm(const mqv_lin_desc* d, int op, const void* a, const void* b,
   g.e = e;
   g.e.vec4 = plan_e.vec4;
   g.e.bias_on_row = plan_e.bias_on_row;
-  g.run = run_length(pl, g.e.d.bf16);
+  g.run = run_length(g.e.d.bf16);
   char* w = static_cast<char*>(ws);
   if (g.splits > 1) g.part = reinterpret_cast<float*>(w);
   w += pl.part_bytes;
@@ -937,7 +942,7 @@ mqv_status mqv_selftest_lin_instance(const mqv_lin_desc* d, int32_t op, int32_t 
   } else {
     GemmPlan pl;
     plan_gemm(d, op, &pl);
-    pl.args.run = run_length(pl, out_type == MQV_BF16 && op != MQV_OP_WGRAD);
+    pl.args.run = run_length(out_type == MQV_BF16 && op != MQV_OP_WGRAD);
     launch_gemm(pl, GemmMaps{}, to);
   }
   return ok();

@@ -16,6 +16,7 @@ pytestmark = pytest.mark.gpu
 
 KIND = {torch.float32: "f32", torch.bfloat16: "bf16"}
 F32, BF16 = torch.float32, torch.bfloat16
+FWD, WGRAD, DGRAD = mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD
 EPS = float(np.float32(1e-5))          # the descriptor holds fp32
 
 
@@ -238,6 +239,51 @@ def test_products_of_integers_are_exact(shape):
     gw = mqv.lin_wgrad(d, gz, x, gw=poison((Cout, Cin), F32))
     assert torch.equal(gw.double(), gm.t() @ xm)
     assert mqv.device_errors() == 0
+
+
+def _long_sums(op, M, K, N, dtype):
+    """(result [M][N] of positive products over K, its value, both fp64): the
+    case in which every step of a running sum that truncates loses."""
+    g = torch.Generator(device="cuda").manual_seed(K + M)
+    a, b = ((torch.rand((n, K), generator=g, device="cuda") * 0.5 + 0.5).to(BF16) for n in (M, N))
+    ref = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for k in range(0, K, 8192):
+        ref += a[:, k:k + 8192].double() @ b[:, k:k + 8192].double().t()
+    d = {FWD: mqv.lin_desc(M, K, N), DGRAD: mqv.lin_desc(M, N, K), WGRAD: mqv.lin_desc(K, N, M)}[op]
+    # the whole of K in one tile's accumulator, or in its runs
+    assert "split" not in mqv.selftest_lin_instance(d, op, dtype)
+    if op == FWD:
+        y, _ = mqv.lin_fwd(d, b, a, y_dtype=dtype)
+    elif op == DGRAD:
+        y = mqv.lin_dgrad(d, b.t().contiguous(), a, gx_dtype=dtype)
+    else:
+        y = mqv.lin_wgrad(d, a.t().contiguous(), b.t().contiguous())
+    assert mqv.device_errors() == 0
+    return y.view(M, N).double(), ref
+
+
+@pytest.mark.parametrize("op", [FWD, DGRAD, WGRAD])
+@pytest.mark.parametrize("M,N", [(2048, 1280), (1999, 1283)])
+def test_long_sums_in_fp32(op, M, N):
+    """Within (64 + K / 512)·2^-24 of the sum: an accumulator takes 32 steps of
+    16 products and loses at most a step of the sum, 2·2^-24, at each; the
+    runs are added to nearest, a rounding of 2^-24 each."""
+    K = 8192
+    y, ref = _long_sums(op, M, K, N, F32)
+    worst = float(((y - ref).abs() / ref).max())
+    assert worst <= (64 + K / 512) * 2.0 ** -24
+
+
+def test_long_sums_in_bfloat16():
+    """Half a step of bfloat16, and what the fp32 sum may be off by: runs of
+    32768 products, 2048 steps of at most 2·2^-24 of a sum that grows evenly,
+    2048·2^-24 of it, and a rounding for each run."""
+    K = 1 << 18
+    y, ref = _long_sums(FWD, 2048, K, 1280, BF16)
+    err = (2048 + K / 32768) * 2.0 ** -24 * ref
+    half = torch.exp2(torch.floor(torch.log2(ref + err)) - 8)
+    worst = float(((y - ref).abs() / (half + err)).max())
+    assert worst <= 1
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
@@ -577,9 +623,6 @@ def _guarded(call, need, kind):
     for bad in (buf[1024:1024 + need - 1], buf[1032:1032 + need]):
         with pytest.raises(mqv.MqvError):
             call(bad)
-
-
-FWD, WGRAD, DGRAD = mqv.OP_FWD, mqv.OP_WGRAD, mqv.OP_DGRAD
 
 
 @pytest.mark.parametrize("shape,ops", [
