@@ -491,7 +491,8 @@ mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, f
  * bounded waits inside the conv and linear-layer kernels set when they give up
  * (*flags = 0: none).  Returns MQV_ERR_TIMEOUT if a flag was set.  Bits:
  * 1 a wait for a free pipeline stage, 2 a wait for a filled stage, 4 a wait
- * for a finished accumulator, 8 the wait of mqv_selftest_wait_timeout.
+ * for a finished accumulator, 8 and 16 the waits of mqv_selftest_wait_timeout
+ * and mqv_selftest_warp_wait_timeout.
  * Every such wait polls its mbarrier for about 2^32 SM cycles (about two
  * seconds) before it gives up; the kernel then returns without faulting, so
  * the CUDA context stays usable. */
@@ -503,6 +504,11 @@ mqv_status mqv_device_errors(uint32_t* flags, void* stream);
  * word and returns.  Nothing else is touched; mqv_device_errors then returns
  * MQV_ERR_TIMEOUT with that bit.  Not part of the method. */
 mqv_status mqv_selftest_wait_timeout(int64_t limit_cycles, void* stream);
+
+/* The same for the linear layer's bounded wait, in which a warp waits as one;
+ * bit 16 as well if it gives up a barrier that has been arrived at, or does
+ * not give up the other. */
+mqv_status mqv_selftest_warp_wait_timeout(int64_t limit_cycles, void* stream);
 
 /* Test hooks: the kernel instances, as text, that mqv_ln_fwd (bwd = 0) or
  * mqv_ln_bwd, or a product of the linear layer (op = MQV_OP_FWD, MQV_OP_WGRAD

@@ -114,13 +114,13 @@ __device__ __forceinline__ bool elect_one() {
 
 // The whole warp waits, bounded as mbar_wait_bounded, and leaves as one: loads
 // and stores of tensor memory want all of its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
-  constexpr long long kLimit = 1ll << 32;
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
+                                          long long limit = 1ll << 32) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
 #pragma unroll 1
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-    if (__any_sync(0xffffffffu, clock64() - t0 > kLimit)) {
+    if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
       atomicOr(err, code);
       return false;
     }
@@ -597,6 +597,20 @@ __device__ __forceinline__ void gemm_epilogue_any(const GemmTcArgs& g, uint32_t 
     }
     c.next(g, 16);
   }
+}
+
+// warp_wait's timeout on its own: two barriers, one that has been arrived at,
+// which is not to set anything, and one that nothing arrives at.
+__global__ void warp_wait_selftest_kernel(uint32_t* err, uint32_t code, uint32_t wrong, long long limit) {
+  __shared__ uint64_t bars[2];
+  if (threadIdx.x == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    fence_mbar_init();
+    mbar_arrive(bars);
+  }
+  __syncwarp();
+  if (!warp_wait(bars, 0, err, wrong, limit) || warp_wait(bars + 1, 0, err, code, limit)) atomicOr(err, wrong);
 }
 
 template <int BN, bool PAIR>

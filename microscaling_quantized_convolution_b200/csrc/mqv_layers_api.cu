@@ -918,6 +918,16 @@ mqv_status mqv_lin_wgrad(const mqv_lin_desc* d, const void* gz, const void* x, f
   return run_gemm(d, MQV_OP_WGRAD, gz, x, e, ws, static_cast<cudaStream_t>(stream));
 }
 
+mqv_status mqv_selftest_warp_wait_timeout(int64_t limit_cycles, void* stream) {
+  if (limit_cycles < 1 || limit_cycles > (int64_t{1} << 32))
+    return fail(MQV_ERR_INVALID_ARG, "limit_cycles %lld outside 1 .. 2^32", (long long)limit_cycles);
+  uint32_t* err = nullptr;
+  const mqv_status st = device_error_word(&err);
+  if (st) return st;
+  warp_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(err, 8, 16, limit_cycles);
+  return launched("self-test launch");
+}
+
 mqv_status mqv_selftest_ln_instance(const mqv_ln_desc* d, int32_t bwd, char* text, size_t bytes) {
   LnPlan pl;
   const mqv_status st = plan_ln(d, bwd != 0, &pl);

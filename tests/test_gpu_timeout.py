@@ -41,6 +41,27 @@ def test_bounded_wait_gives_up_and_reports():
     assert np.isfinite(mqv.dequantize(q).cpu().numpy()).all()
 
 
+def test_warp_wait_gives_up_and_reports():
+    """The linear layer's wait: gives up after its limit and no earlier, does
+    not give up a barrier that has been arrived at (bit 16), and leaves the
+    product kernel usable."""
+    assert mqv.device_errors() == 0
+    limit = 4_000_000
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    mqv.selftest_warp_wait_timeout(limit)
+    b.record()
+    torch.cuda.synchronize()
+    ms = a.elapsed_time(b)
+    flags = ctypes.c_uint32()
+    st = mqv.lib().mqv_device_errors(ctypes.byref(flags), None)
+    assert st == MQV_ERR_TIMEOUT and flags.value == SELFTEST_BIT
+    assert limit / 2.1e6 <= ms < 1000.0, ms
+    one = torch.ones((64, 64), dtype=torch.bfloat16, device="cuda")
+    y, _ = mqv.lin_fwd(mqv.lin_desc(64, 64, 64), one, one)
+    assert (y == 64).all() and mqv.device_errors() == 0
+
+
 def test_timeout_flag_accumulates_across_calls_until_read():
     mqv.device_errors()
     mqv.selftest_wait_timeout(100_000)

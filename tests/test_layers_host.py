@@ -224,6 +224,11 @@ def test_instance_hooks_refuse_what_the_calls_refuse():
     assert text.value == b"lau"                                   # cut off within its size
 
 
+@pytest.mark.parametrize("bad", [0, -1, (1 << 32) + 1])
+def test_warp_wait_limit_is_validated(bad):
+    assert mqv.lib().mqv_selftest_warp_wait_timeout(bad, None) == 1
+
+
 # addresses of pretend buffers, far enough apart for the shapes used here;
 # each call below is refused before anything is launched
 A = [1 << 20 << i for i in range(10)]
