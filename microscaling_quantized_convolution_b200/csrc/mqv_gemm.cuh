@@ -708,6 +708,12 @@ gemm_tc_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ Ge
         const int fills = static_cast<int>(round) + (j < s);
         if (fills > 0) warp_wait(full + j, (fills - 1) & 1, g.err, 2);
       }
+    // the last release of each stage is an arrival on this CTA's barriers, from
+    // the other one's products in a pair: it is waited for before they go
+    for (int j = 0; j < kStages && live; ++j) {
+      const int fills = static_cast<int>(round) + (j < s);
+      if (fills > 0) live = warp_wait(empty + j, (fills - 1) & 1, g.err, 1);
+    }
   } else if (warp == 1 && rank == 0) {
     // ---- MMA issuer
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(g.a.mn_major) << 15) |
