@@ -45,6 +45,9 @@ LIN_PAIR = [(245, 520, 1248, 4), (285, 1049, 803, 4), (238, 656, 760, 8), (300, 
 LIN_FEW = [(1, 5, 7, 1), (1, 2056, 40, 1), (1, 4099, 33, 1), (2, 7, 5, 1), (2, 1001, 1003, 1), (2, 4104, 24, 1),
            (3, 24, 41, 1), (3, 2048, 96, 1), (3, 4099, 33, 1), (4, 5, 7, 1), (4, 136, 72, 1), (4, 1003, 1001, 1),
            (4, 4096, 520, 1)]
+# one channel on a side, one column
+LIN_THIN = [(5000, 64, 1, 1), (3000, 1, 65, 1), (2500, 1, 1, 1), (700, 1, 1, 16), (1, 4096, 1, 64), (2, 1, 5, 1000),
+            (1, 1, 4099, 4), (40, 300, 1, 3), (1, 3, 2, 2049)]
 # either side of the change to 1024 threads a tile
 LN_WIDE_TILES = [(2, 1024, 16), (2, 1025, 16), (4, 1500, 16), (4, 2048, 16), (3, 2000, 12), (5, 1100, 12), (2, 1400, 12),
                  (300, 1032, 16)]

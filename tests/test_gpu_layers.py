@@ -1,6 +1,8 @@
 """GPU parity of the layer norm and the linear layer against their fp64
 definitions, every output within the oracle's error bound, the same bits on a
 second run; streams, graphs, in-place forms, special values and refusals."""
+import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
@@ -9,8 +11,9 @@ import torch
 
 import microscaling_quantized_convolution_b200 as mqv
 from oracle import layers_oracle as L
-from tests.layers_cases import (LIN_FEW, LIN_LONG, LIN_PAIR, LIN_PIXELS, LIN_TOKENS, LIN_WIDE, LN_ROWS, LN_TILES,
-                                LN_WIDE_TILES, activations, shape_id, stored)
+from tests.conftest import ROOT
+from tests.layers_cases import (LIN_FEW, LIN_LONG, LIN_PAIR, LIN_PIXELS, LIN_THIN, LIN_TOKENS, LIN_WIDE, LN_ROWS,
+                                LN_TILES, LN_WIDE_TILES, activations, shape_id, stored)
 
 pytestmark = pytest.mark.gpu
 
@@ -214,7 +217,8 @@ def _integers(shape, limit, g):
     return torch.randint(-limit, limit + 1, shape, generator=g, device="cuda").to(BF16)
 
 
-@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG + LIN_PAIR + LIN_FEW, ids=shape_id)
+@pytest.mark.parametrize("shape", LIN_TOKENS + LIN_PIXELS + LIN_WIDE + LIN_LONG + LIN_PAIR + LIN_FEW + LIN_THIN,
+                         ids=shape_id)
 def test_products_of_integers_are_exact(shape):
     """Small integers: every sum of products, in any order, is an integer below
     2^24 that fp32 holds (9 times at most 12500 terms), so the results have one
@@ -238,6 +242,38 @@ def test_products_of_integers_are_exact(shape):
         assert torch.equal(rows(gx), (gm @ w.double()).to(dtype).double())
     gw = mqv.lin_wgrad(d, gz, x, gw=poison((Cout, Cin), F32))
     assert torch.equal(gw.double(), gm.t() @ xm)
+    assert mqv.device_errors() == 0
+
+
+@pytest.mark.parametrize("shape", [
+    (596, 531, 3752, 1), (513, 3778, 546, 1), (134, 2456, 3168, 1), (245, 520, 1248, 4), (300, 585, 739, 8),
+    (332, 152, 2040, 8), (1280, 1100, 1000, 1), (65, 1992, 2500, 1), (130, 72, 136, 1), (300, 264, 520, 32),
+    (7, 16, 8, 4), (10, 24, 24, 8), (9, 48, 72, 20), (6, 65, 63, 16), (64, 4096, 256, 1), (33, 3001, 257, 1),
+    (1, 2056, 40, 1), (3, 4099, 33, 1), (4, 136, 72, 1)], ids=shape_id)
+def test_every_epilogue_of_integers_is_exact(shape):
+    """Each of bias, residual and kept pre-activation with and without the
+    others, without an activation and with ReLU, in fp32 and bfloat16: all
+    integers that fp32 holds, so each result has one value."""
+    P, Cin, Cout, N = shape
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    w, x = _integers((Cout, Cin), 3, g), _integers((P, Cin, N), 3, g)
+    bias, res = _integers((Cout,), 50, g).float(), _integers((P, Cout, N), 50, g)
+    sums = torch.einsum("oi,pin->pon", w.double(), x.double())
+    for act in ("none", "relu"):
+        d = mqv.lin_desc(*shape, act)
+        for with_bias in (False, True):
+            z = sums + bias.double()[:, None] if with_bias else sums
+            a = z.clamp(min=0) if act == "relu" else z
+            for with_res in (False, True):
+                for dtype in (F32, BF16):
+                    for keep in (False, True):
+                        y, kept = mqv.lin_fwd(d, w, x, bias=bias if with_bias else None,
+                                              residual=res.to(dtype) if with_res else None, y_dtype=dtype,
+                                              y=poison((P, Cout, N), dtype), z=poison((P, Cout, N), BF16) if keep else None)
+                        what = (act, with_bias, with_res, dtype, keep)
+                        want = a + res.double() if with_res else a
+                        assert torch.equal(y.double(), want.to(dtype).double()), what
+                        assert not keep or torch.equal(kept.double(), z.to(BF16).double()), what
     assert mqv.device_errors() == 0
 
 
@@ -489,6 +525,38 @@ def test_block_on_another_stream_and_in_a_graph(shape):
     fresh = _block(d1, d2, ln, t, x)
     for k in want:
         assert torch.equal(graphs[0][1][k], fresh[k]), k
+
+
+_FIRST = """
+import torch, microscaling_quantized_convolution_b200 as mqv
+P, C, H, N = {shape}
+x, w = torch.ones((P, C, N), device="cuda"), torch.ones((H, C), dtype=torch.bfloat16, device="cuda")
+ln, d = mqv.ln_desc(P, C, N), mqv.lin_desc(P, C, H, N, "gelu")
+x[:, 0] = 3.0
+torch.cuda.synchronize()
+def passes():
+    h, mean, rstd = mqv.ln_fwd(ln, x, y_dtype=torch.bfloat16)
+    y, z = mqv.lin_fwd(d, w, h, save_z=True)
+    gz, gb = mqv.lin_act_grad(d, y, z)
+    gx = mqv.lin_dgrad(d, w, gz)
+    return (h, y, z, gz, gb, gx, mqv.lin_wgrad(d, gz, h)) + mqv.ln_bwd(ln, gx, x, mean, rstd)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = passes()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, passes(), strict=True))
+assert mqv.device_errors() == 0
+"""
+
+
+@pytest.mark.parametrize("shape", [(300, 72, 136, 1), (9, 24, 56, 12), (2048, 1024, 2048, 1)], ids=shape_id)
+def test_first_calls_of_a_process_are_captured(shape):
+    """Nothing that a first call sets up (kernel attributes, the error word, the
+    tensor map encoder) is refused under capture."""
+    run = subprocess.run([sys.executable, "-c", _FIRST.format(shape=shape)], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 def test_block_from_several_host_threads():
