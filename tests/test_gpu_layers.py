@@ -142,6 +142,37 @@ def test_layer_norm_special_columns(shape):
         check(y[:, :, 1:].contiguous(), ref["y"], "y")
 
 
+@pytest.mark.parametrize("shape", [(6, 320, 1), (6, 33, 1), (700, 264, 1), (6, 48, 16), (5, 20, 12), (4, 1500, 16),
+                                   (4, 5000, 3), (4, 700, 63), (4, 128, 64)], ids=shape_id)
+def test_layer_norm_gradients_of_special_columns(shape):
+    """Infinities and NaN in gy, x or the statistics of a column spoil that
+    column's gx and no other, bit for bit, and reach ggamma and gbeta only in
+    the channels that have them (x and the statistics: ggamma)."""
+    P, C, N = shape
+    x, gamma, beta, gy = ln_inputs(shape)
+    d, gam = mqv.ln_desc(*shape), dev(gamma)
+    xd, gyd = dev(x), dev(gy)
+    _, mean, rstd = mqv.ln_fwd(d, xd, gam, dev(beta))
+    want, wg, wb = mqv.ln_bwd(d, gyd, xd, mean, rstd, gam)
+    n = N - 1
+    gyd[1, 2, n], gyd[2, C - 1, 0] = float("nan"), float("inf")
+    gx, gg, gb = mqv.ln_bwd(d, gyd, xd, mean, rstd, gam)
+    bad = torch.zeros((P, N), dtype=torch.bool, device="cuda")
+    bad[1, n] = bad[2, 0] = True
+    assert not torch.isfinite(gx).all(1)[bad].any()
+    assert torch.equal(gx.transpose(1, 2)[~bad], want.transpose(1, 2)[~bad])
+    odd = torch.zeros(C, dtype=torch.bool, device="cuda")
+    odd[2] = odd[C - 1] = True
+    for got, ref in ((gg, wg), (gb, wb)):
+        assert not torch.isfinite(got[odd]).any() and torch.equal(got[~odd], ref[~odd])
+    gyd = dev(gy)
+    xd[1, 2, n] = float("nan")
+    mean[2, 0], rstd[2, 0] = float("nan"), float("inf")
+    gx, gg, gb = mqv.ln_bwd(d, gyd, xd, mean, rstd, gam)
+    assert torch.equal(gx.transpose(1, 2)[~bad], want.transpose(1, 2)[~bad]) and torch.equal(gb, wb)
+    assert torch.isnan(gx[1, :, n]).all() and torch.isnan(gg).all()
+
+
 @pytest.mark.parametrize("shape,rows,per_warp", [((1, 16384, 4), 1024, 32), ((1, 4096, 8), 512, 16)])
 def test_layer_norm_sums_take_no_more_additions_than_bounded(shape, rows, per_warp):
     """A one, and in every place where a partial sum that holds it takes
