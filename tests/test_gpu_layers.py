@@ -463,6 +463,44 @@ def test_infinite_inputs_stay_in_their_outputs():
         assert torch.equal(b[fine], y[fine])
 
 
+@pytest.mark.parametrize("shape", [(70, 128, 136, 1), (90, 73, 41, 1), (3, 64, 48, 16), (5, 33, 40, 12), (4, 31, 37, 7),
+                                   (3, 4099, 33, 1), (4, 136, 72, 1), (596, 531, 3752, 1), (300, 585, 739, 8),
+                                   (1280, 1100, 1000, 1), (65, 1992, 2500, 1)], ids=shape_id)
+def test_special_values_stay_in_their_sums(shape):
+    """A NaN or infinity in w, x or gz reaches the results whose sums have it,
+    whatever lies beside it in memory, and no other, bit for bit."""
+    P, Cin, Cout, N = shape
+    w, x, bias, _, gy = lin_inputs(shape)
+    wd, xd, bd, gd = dev(w, BF16), dev(x, BF16), dev(bias), dev(gy, BF16)
+    d = mqv.lin_desc(*shape)
+    y, gx, gw = mqv.lin_fwd(d, wd, xd, bd)[0], mqv.lin_dgrad(d, wd, gd), mqv.lin_wgrad(d, gd, xd)
+    # the last values of a row, and the first of the next
+    w2, x2, g2 = wd.clone(), xd.clone(), gd.clone()
+    w2[1, Cin - 1], w2[2, 0] = float("nan"), float("inf")
+    x2[P // 2, Cin - 1, N - 1], x2[P - 1, 0, 0] = float("inf"), float("nan")
+    g2[P // 2, Cout - 1, N - 1], g2[P - 1, 0, 0] = float("nan"), float("-inf")
+    cols = torch.zeros((P, N), dtype=torch.bool, device="cuda")
+    cols[P // 2, N - 1] = cols[P - 1, 0] = True
+
+    def spoiled(got, want, where):
+        """where: of got's shape, true where a value has to be spoiled."""
+        where = where.expand(got.shape)
+        assert not torch.isfinite(got[where]).any() and torch.equal(got[~where], want[~where])
+
+    def channels(n, *which):
+        m = torch.zeros(n, dtype=torch.bool, device="cuda")
+        m[list(which)] = True
+        return m
+
+    spoiled(mqv.lin_fwd(d, w2, xd, bd)[0], y, channels(Cout, 1, 2)[:, None])
+    spoiled(mqv.lin_dgrad(d, w2, gd), gx, channels(Cin, 0, Cin - 1)[:, None])
+    spoiled(mqv.lin_fwd(d, wd, x2, bd)[0], y, cols[:, None])
+    spoiled(mqv.lin_dgrad(d, wd, g2), gx, cols[:, None])
+    spoiled(mqv.lin_wgrad(d, gd, x2), gw, channels(Cin, 0, Cin - 1))
+    spoiled(mqv.lin_wgrad(d, g2, xd), gw, channels(Cout, 0, Cout - 1)[:, None])
+    assert mqv.device_errors() == 0
+
+
 # ----------------------------------- streams, graphs, workspaces, refusals
 
 def _block(d1, d2, ln, t, x, **kw):
