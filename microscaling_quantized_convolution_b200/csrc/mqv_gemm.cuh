@@ -25,10 +25,13 @@
 // Everything outside the view reads as zero, in both operands.
 //
 // What bounds it: with many K blocks the operand bytes that come from L2 (a CTA
-// takes 32 KB a K block, about 0.32 us whatever the tile, so the pair's tile,
-// with twice the products for them, is the fast one: 8192 tokens 4096 -> 4096
-// in 164 us, 1.67 PFLOP/s, 0.98 of the measured bfloat16 rate); with few the
-// epilogue (4 us for a 256 x 256 tile).
+// takes 32 KB a K block for its part of the pair's tile and for a 128 x 128
+// tile, 24 KB for a 128 x 64 one, in 0.34, 0.28 and 0.255 us, so the pair's
+// tile, with two to four times the products for them, is the fast one: 8192
+// tokens 4096 -> 4096 from a cold L2 in 165 us, 1.67 PFLOP/s, 0.98 of the
+// measured bfloat16 burst rate; one after another under the power cap 215 us,
+// as cuBLAS); with few the epilogue (a 256 x 256 tile 4.1 us, about 9.3 with
+// GELU and a kept pre-activation).
 //
 // Outputs.  FAST, when the output's rows are 16-byte aligned: an epilogue
 // thread has 32 columns of one row in registers; bias and activation are

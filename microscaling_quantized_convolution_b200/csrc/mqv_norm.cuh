@@ -26,7 +26,7 @@
 // parameter gradients in registers; a block adds its groups' in order and
 // writes one partial row, and column_sum_kernel adds the rows in a fixed order.
 //
-// Measured, L2 flushed: forward 16384 x 4096 bfloat16 47 us (5.7 TB/s, 0.89 of
+// Measured, L2 flushed: forward 16384 x 4096 bfloat16 47 us (5.7 TB/s, 0.88 of
 // the copy rate), 80 x 80 pixels of 64 channels at batch 16, fp32 to bfloat16,
 // 8.7 us (0.72); backward 8192 x 4096 50 us (4.0 TB/s, 0.62: instruction issue
 // and latency at the 512 threads an SM that the registers allow), 56 x 56
@@ -34,6 +34,9 @@
 // tiles a group: the last round is not full).  8 instead of 16 values a thread
 // at twice the threads are slower (64 us for 8192 x 4096 backward), so are 80
 // registers for a third block (76 us, spills), or a prefetch of tiles (no gain).
+// The backward instances of 1024 threads (rows of more than 8192 channels and
+// the tiles beside them) have 64 registers and spill, 372 to 1124 bytes a
+// thread: 3000 x 16384 196 us, where the bytes take 46.
 #pragma once
 
 #include "mqv_layer_common.cuh"
